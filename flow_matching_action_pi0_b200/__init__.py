@@ -8,7 +8,8 @@ fallback path.
 Functions keep the C names (pae_create, pae_set_prefix, pae_set_prefix_hidden,
 pae_precompute_tables,
 pae_denoise, pae_denoise_host, pae_denoise_steps, pae_sync, ...).  The
-ActionExpert class wraps a context for convenience.
+ActionExpert class wraps a context for convenience; quantize_rows, linear_i8
+and KvCacheInt8 (int8.py) take tensors for the 8-bit prefix operators.
 """
 from __future__ import annotations
 
@@ -39,7 +40,8 @@ STATUS_NAMES = {0: "PAE_OK", 1: "PAE_ERR_ARG", 2: "PAE_ERR_STATE", 3: "PAE_ERR_C
 EXPORTS = ("pae_create", "pae_set_prefix", "pae_set_prefix_hidden", "pae_precompute_tables", "pae_denoise", "pae_denoise_host",
            "pae_denoise_steps", "pae_set_option", "pae_profile_read", "pae_query", "pae_plan_query", "pae_sync",
            "pae_clear_error", "pae_last_error", "pae_debug_copy", "pae_precompute_tables_static",
-           "pae_destroy")
+           "pae_int8_init", "pae_int8_sync", "pae_int8_clear_error", "pae_quantize_rows", "pae_linear_i8",
+           "pae_kv8_write", "pae_kv8_read", "pae_kv8_workspace", "pae_kv8_attention", "pae_destroy")
 
 
 class PaeError(RuntimeError):
@@ -67,6 +69,18 @@ class pae_weights(ctypes.Structure):
                                    "s_qkv", "s_o", "s_gate", "s_up", "s_down", "w_prefix_kv")]
 
 
+class pae_kv8(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(n, ctypes.c_int) for n in ("n_slots", "n_kv_heads", "capacity", "head_dim")]
+
+
+class pae_kv8_query(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("lens", "q", "out", "k_new", "v_new")] + \
+               [(n, ctypes.c_longlong * 3) for n in ("q_strides", "out_strides", "k_new_strides", "v_new_strides")] + \
+               [(n, ctypes.c_int) for n in ("n_seq", "n_q", "n_q_heads", "n_new", "causal")] + \
+               [("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -79,6 +93,7 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -m flow_matching_action_pi0_b200.build`")
     L = ctypes.CDLL(LIB_PATH)
     i, v, vp, st = ctypes.c_int, ctypes.c_void_p, _PP, ctypes.c_void_p
+    ll, pll, kv = ctypes.c_longlong, ctypes.POINTER(ctypes.c_longlong), ctypes.POINTER(pae_kv8)
     sig = {
         "pae_create": (i, [ctypes.POINTER(pae_config), ctypes.POINTER(pae_weights), ctypes.POINTER(v)]),
         "pae_set_prefix": (i, [v, i, vp, vp, i, st]),
@@ -98,6 +113,15 @@ def lib() -> ctypes.CDLL:
         "pae_destroy": (None, [v]),
         "pae_precompute_tables_static": (i, [i, i, i, ctypes.POINTER(pae_weights), ctypes.POINTER(ctypes.c_double),
                                              i, v, v, st]),
+        "pae_int8_init": (i, []),
+        "pae_int8_sync": (i, [st]),
+        "pae_int8_clear_error": (None, []),
+        "pae_quantize_rows": (i, [v, ll, i, i, i, ctypes.c_float, v, v, st]),
+        "pae_linear_i8": (i, [v, v, v, v, i, i, i, v, ll, i, st]),
+        "pae_kv8_write": (i, [kv, v, v, pll, pll, v, v, i, i, i, st]),
+        "pae_kv8_read": (i, [kv, v, v, pll, pll, v, v, i, i, i, st]),
+        "pae_kv8_workspace": (i, [kv, i, i, i, i, ctypes.POINTER(ctypes.c_size_t)]),
+        "pae_kv8_attention": (i, [kv, ctypes.POINTER(pae_kv8_query), v, ctypes.c_size_t, st]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -210,6 +234,56 @@ def pae_precompute_tables_static(layers: int, width: int, dtype: int, weights: p
                                               dt_ptr, _stream(stream)))
 
 
+def pae_int8_init():
+    _check(lib().pae_int8_init())
+
+
+def pae_int8_sync(stream=None):
+    _check(lib().pae_int8_sync(_stream(stream)))
+
+
+def pae_int8_clear_error():
+    lib().pae_int8_clear_error()
+
+
+def _ll_array(values: Optional[Sequence[int]]):
+    return None if values is None else (ctypes.c_longlong * len(values))(*values)
+
+
+def pae_quantize_rows(x_ptr: int, ldx: int, rows: int, width: int, dtype: int, rms_eps: float, codes_ptr: int,
+                      scale_ptr: int, stream=None):
+    _check(lib().pae_quantize_rows(x_ptr, ldx, rows, width, dtype, rms_eps, codes_ptr, scale_ptr, _stream(stream)))
+
+
+def pae_linear_i8(x_ptr: int, x_scale_ptr: int, w_ptr: int, w_scale_ptr: int, tokens: int, n: int, k: int, y_ptr: int,
+                  ldy: int, dtype: int, stream=None):
+    _check(lib().pae_linear_i8(x_ptr, x_scale_ptr, w_ptr, w_scale_ptr, tokens, n, k, y_ptr, ldy, dtype,
+                               _stream(stream)))
+
+
+def pae_kv8_write(cache: pae_kv8, k_ptr: int, v_ptr: int, k_strides, v_strides, cu_ptr, start_ptr, n_seq: int,
+                  n_rows: int, dtype: int, stream=None):
+    _check(lib().pae_kv8_write(ctypes.byref(cache), k_ptr, v_ptr, _ll_array(k_strides), _ll_array(v_strides), cu_ptr,
+                               start_ptr, n_seq, n_rows, dtype, _stream(stream)))
+
+
+def pae_kv8_read(cache: pae_kv8, k_ptr: int, v_ptr: int, k_strides, v_strides, cu_ptr, start_ptr, n_seq: int,
+                 n_rows: int, dtype: int, stream=None):
+    _check(lib().pae_kv8_read(ctypes.byref(cache), k_ptr, v_ptr, _ll_array(k_strides), _ll_array(v_strides), cu_ptr,
+                              start_ptr, n_seq, n_rows, dtype, _stream(stream)))
+
+
+def pae_kv8_workspace(cache: pae_kv8, n_seq: int, n_q: int, n_q_heads: int, n_new: int = 0) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().pae_kv8_workspace(ctypes.byref(cache), n_seq, n_q, n_q_heads, n_new, ctypes.byref(n)))
+    return n.value
+
+
+def pae_kv8_attention(cache: pae_kv8, query: pae_kv8_query, workspace_ptr, workspace_bytes: int, stream=None):
+    _check(lib().pae_kv8_attention(ctypes.byref(cache), ctypes.byref(query), workspace_ptr, workspace_bytes,
+                                   _stream(stream)))
+
+
 def pae_destroy(ctx: int):
     if ctx:
         lib().pae_destroy(ctx)
@@ -306,3 +380,11 @@ class ActionExpert:
 
     def debug_copy(self, name: str):
         return pae_debug_copy(self.ctx, name)
+
+
+def __getattr__(name):
+    # the tensor-level 8-bit operators; int8.py imports torch, this module alone does not
+    if name in ("quantize_rows", "linear_i8", "KvCacheInt8", "Kv8Plan"):
+        from . import int8
+        return getattr(int8, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

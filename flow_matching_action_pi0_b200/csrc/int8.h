@@ -1,0 +1,94 @@
+// Launch interface of the 8-bit prefix operators (row quantiser, int8
+// product, int8 K/V cache, attention over that cache), shared by their entry
+// points (pae_int8.cu) and the context (pae_api.cu).  Host-side declarations.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace pae {
+
+// ------------------------------------------------------------ row quantiser
+// codes[r][i] = rint(x[r][i] / s_r), s_r = max|x[r]| / 127; scale[r] = s_r, or
+// with rms_eps > 0 s_r / sqrt(mean(x[r]^2) + rms_eps): the codes of the
+// normalised row are the same, only its scale changes.
+cudaError_t launch_quantize_rows(bool in_bf16, const void* x, long long ldx, int rows, int width, float rms_eps,
+                                 int8_t* codes, float* scale, cudaStream_t st);
+
+// ------------------------------------------------------------- int8 product
+// y[t][f] = (sum_k x[t][k] w[f][k]) sx[t] sw[f], int32 sums.
+struct I8GemmPlan {
+  int swap;     // 1: weight rows on the MMA's M side, tokens on its N side
+  int tn;       // N tile (multiple of 16, 16..256)
+  int tiles_m, tiles_n;
+  int splits;   // split-K cluster size (swap only)
+  int stages;
+  int ctas;     // persistent grid (swap == 0)
+};
+I8GemmPlan plan_i8_gemm(int tokens, int n, int k);
+struct I8GemmArgs {
+  const float* sx;
+  const float* sw;
+  void* y;
+  long long ldy;
+  int tokens, n, k;
+  DevErr err;
+};
+cudaError_t i8_gemm_init();
+cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols, const I8GemmPlan& p,
+                           const I8GemmArgs& a, cudaStream_t st);
+
+// ---------------------------------------------------------------- K/V cache
+struct Kv8 {
+  int8_t *k, *v;            // [slots][heads][cap][d]
+  float *k_scale, *v_scale; // [slots][heads][cap]
+  int slots, heads, cap, d;
+};
+struct Kv8Rows {            // packed rows of n_seq sequences: sequence b is rows [cu[b], cu[b + 1])
+  const int* cu;            // [n_seq + 1]; null: one sequence of n_rows rows
+  const int* start;         // [n_seq] position of each sequence's first row; null: 0
+  int n_seq, n_rows, slot0; // sequence b goes to slot slot0 + b
+};
+struct Kv8Io {              // row (t, head) at p + t * tok + head * head_stride (elements)
+  void *k, *v;
+  long long k_tok, k_head, v_tok, v_head;
+};
+cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
+cudaError_t launch_kv8_read(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention
+constexpr int kMaxKv8Splits = 128;
+struct Kv8AttnPlan {
+  int tc;        // 1: tcgen05 tiles of 128 query rows; 0: groups of 8 rows
+  int qtiles;    // row tiles (tc) or row groups per (sequence, KV head)
+  int splits;    // key splits; > 1: partial rows go to the workspace and are merged by a second launch
+  size_t ws_bytes;
+};
+Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new, int max_keys, int d);
+struct Kv8AttnArgs {
+  Kv8 c;
+  const int* lens;          // [n_seq] valid cached positions of slot b
+  const bf16* q;            // strides in elements
+  long long q_seq, q_tok, q_head;
+  bf16* o;
+  long long o_seq, o_tok, o_head;
+  const bf16 *k_new, *v_new;  // fresh keys, visible to every query (null: none)
+  long long kn_seq, kn_tok, kn_head, vn_seq, vn_tok, vn_head;
+  int n_seq, n_q, n_new, group;  // group = query heads per KV head
+  int causal;
+  float scale_log2;         // softmax scale x log2(e)
+  float* part_o;            // [n_seq * heads][splits][rows][d] unnormalised rows
+  float2* part_ml;          // [n_seq * heads][splits][rows] (max in the log2 domain, sum)
+  DevErr err;
+};
+cudaError_t kv8_attn_init();
+cudaError_t launch_kv8_attn(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st);
+
+// parts of launch_kv8_attn
+cudaError_t kv8_attn_tc_init();
+cudaError_t launch_kv8_attn_tc(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st);
+
+}  // namespace pae

@@ -1,0 +1,513 @@
+// Product of 8-bit integer matrices with one scale per token and per output
+// channel:
+//   y[t][f] = (sum_k x[t][k] w[f][k]) sx[t] sw[f]
+// on the tcgen05 tensor cores (kind::i8: signed 8-bit operands, 32-bit sums in
+// TMEM).  The sums are exact for k <= 131071 (|code| <= 128), so any order
+// and any split of k gives the same bits; the two scales are applied in fp32
+// and the result is rounded once to the output type.
+//
+// Two forms of one tile product D[128 rows][tn columns], chosen by the number
+// of tokens:
+//   tokens on the rows   (many tokens) a persistent grid walks the tiles; the
+//                        accumulator is double-buffered in TMEM, so the
+//                        epilogue of a tile runs under the next one's MMAs
+//   weights on the rows  (few tokens: streaming the weights is what bounds
+//                        it) tokens pad only to a multiple of 16; the k range
+//                        of a tile is split over a cluster of CTAs so that all
+//                        SMs stream weights, and the int32 partials are summed
+//                        through distributed shared memory
+// Warp 0 streams both operands by TMA in 128-byte k blocks (128-byte swizzle)
+// through a ring of stages, warp 1 issues the MMAs (K = 32 codes each), warps
+// 4-7 read the accumulator (thread = TMEM lane = row).
+#include <algorithm>
+
+#include "int8.h"
+#include "launch.cuh"
+
+namespace pae {
+
+namespace {
+
+constexpr long long kDrainNs = 4000000000LL;
+constexpr int KB = 128;  // k block: one 128-byte swizzled row
+
+// D[tmem] (+)= A[smem] B[smem]^T, signed 8-bit inputs, int32 accumulate.
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::i8: D format [4,6) = 2 (s32), A [7,10) = B
+// [10,13) = 1 (signed), both K-major, N>>3 at [17,23), M>>4 at [24,29).
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tmem_ld16i(uint32_t taddr, int* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void reg_fence16i(int* v) {
+  asm volatile(""
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                 "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]));
+}
+
+__host__ __device__ inline uint32_t stage_bytes(int tn) { return 128u * KB + (uint32_t)tn * KB; }
+
+__host__ __device__ inline uint32_t tmem_cols(int n) {
+  uint32_t c = 32;
+  while ((int)c < n) c <<= 1;
+  return c;
+}
+
+// Shared memory: ring | barriers | per-tile column scales / int32 partials.
+struct I8Smem {
+  uint32_t bar_off, sw_off, part_off, total;
+};
+__host__ __device__ inline I8Smem i8_layout(const I8GemmPlan& p) {
+  I8Smem L;
+  L.bar_off = stage_bytes(p.tn) * (uint32_t)p.stages;
+  L.sw_off = L.bar_off + 512;
+  L.part_off = L.sw_off + 2 * 256 * 4;
+  L.total = L.part_off + (p.swap && p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u) + 1024;
+  return L;
+}
+
+template <typename TO>
+__device__ __forceinline__ void st_out(TO* p, float v);
+template <>
+__device__ __forceinline__ void st_out<float>(float* p, float v) { *p = v; }
+template <>
+__device__ __forceinline__ void st_out<bf16>(bf16* p, float v) { *p = f2bf(v); }
+
+// 16 consecutive outputs of one row; `n` of them exist.
+__device__ __forceinline__ void store16(float* p, const float* v, int n, bool vec) {
+  if (vec && n >= 16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+__device__ __forceinline__ void store16(bf16* p, const float* v, int n, bool vec) {
+  if (vec && n >= 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (uint32_t)__bfloat16_as_ushort(f2bf(v[2 * i])) | ((uint32_t)__bfloat16_as_ushort(f2bf(v[2 * i + 1])) << 16);
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = f2bf(v[i]);
+  }
+}
+
+// ------------------------------------------------------- tokens on the rows
+template <typename TO>
+__global__ void __launch_bounds__(256, 1)
+    k_i8_gemm(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC, const I8GemmPlan p,
+              const I8GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const I8Smem L = i8_layout(p);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bar_off);
+  uint64_t* empty = full + p.stages;
+  uint64_t* acc_full = empty + p.stages;  // [2]
+  uint64_t* acc_empty = acc_full + 2;     // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_sw = reinterpret_cast<float*>(smem + L.sw_off);  // [2][256]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nkb = (a.k + KB - 1) / KB;
+  const int tiles = p.tiles_m * p.tiles_n;
+  const uint32_t ncols = tmem_cols(2 * p.tn);
+  const uint32_t sbytes = stage_bytes(p.tn);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 128);
+    }
+    s_flag[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmR);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, ncols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();  // the token codes and scales come from the quantiser
+
+  if (warp == 0 && lane == 0) {
+    int it = 0;
+    bool good = true;
+    for (int tile = blockIdx.x; tile < tiles && good; tile += gridDim.x) {
+      const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        const int st = it % p.stages;
+        if (it >= p.stages && !mbar_wait(&empty[st], ((it / p.stages) & 1) ^ 1, a.err.wait_ns)) {
+          s_flag[0] = 1;
+          set_error(a.err, DEV_TIMEOUT);
+          good = false;
+          break;
+        }
+        uint8_t* s = smem + (size_t)st * sbytes;
+        mbar_arrive_expect_tx(&full[st], sbytes);
+        tma_load_2d(s, &tmR, kb * KB, tm * 128, &full[st]);
+        tma_load_2d(s + 128 * KB, &tmC, kb * KB, tn * p.tn, &full[st]);
+      }
+    }
+    // loads still in flight must land before this CTA may exit
+    for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
+      if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_i8(128, p.tn);
+    int it = 0, n = 0;
+    bool good = true;
+    for (int tile = blockIdx.x; tile < tiles && good; tile += gridDim.x, ++n) {
+      const int buf = n & 1;
+      if (n >= 2 && !mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, a.err.wait_ns)) good = false;
+      for (int kb = 0; kb < nkb && good; ++kb, ++it) {
+        const int st = it % p.stages;
+        if (!mbar_wait(&full[st], (it / p.stages) & 1, a.err.wait_ns)) {
+          good = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t sa = smem_u32(smem + (size_t)st * sbytes);
+        const uint64_t ad = sw128_desc(sa, 16, 1024), bd = sw128_desc(sa + 128 * KB, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < KB / 32; ++kk)
+          umma_i8(tmem + buf * p.tn, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, (kb | kk) != 0 ? 1u : 0u);
+        umma_commit(&empty[st]);
+      }
+      if (good) umma_commit(&acc_full[buf]);
+    }
+    if (!good) {
+      s_flag[0] = 1;
+      set_error(a.err, DEV_TIMEOUT);
+    }
+    // every MMA this thread issued must finish before TMEM is freed
+    uint64_t* drain = reinterpret_cast<uint64_t*>(smem + L.bar_off + 504);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    umma_commit(drain);
+    if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+  } else if (warp >= 4) {
+    const int et = threadIdx.x - 128;  // row of the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    TO* y = static_cast<TO*>(a.y);
+    const bool vec = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && (a.ldy * (long long)sizeof(TO)) % 16 == 0;
+    int n = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+      const int buf = n & 1;
+      const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
+      const int t = tm * 128 + et, f0 = tn * p.tn;
+      float* sw = s_sw + buf * 256;
+      for (int i = et; i < p.tn; i += 128) sw[i] = f0 + i < a.n ? a.sw[f0 + i] : 0.f;
+      const float sx = t < a.tokens ? a.sx[t] : 0.f;
+      // the column scales are in place for all four warps, and all go on or stop
+      const bool got = mbar_wait(&acc_full[buf], (n >> 1) & 1, a.err.wait_ns);
+      __syncwarp();
+      uint32_t go;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t"
+          "setp.ne.u32 p, %1, 0;\n\t"
+          "bar.red.and.pred q, 1, 128, p;\n\t"
+          "selp.u32 %0, 1, 0, q;\n\t}"
+          : "=r"(go)
+          : "r"((uint32_t)(got && s_flag[0] == 0))
+          : "memory");
+      if (!go) {
+        set_error(a.err, DEV_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      int acc[2][16];
+      tmem_ld16i(tmem + buf * p.tn + lane_off, acc[0]);
+      const int nc = p.tn / 16;
+      auto emit = [&](int c, int* v) {
+        if (t < a.tokens && f0 + c * 16 < a.n) {
+          float o[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
+            o[4 * q] = (float)v[4 * q] * sx * w.x;
+            o[4 * q + 1] = (float)v[4 * q + 1] * sx * w.y;
+            o[4 * q + 2] = (float)v[4 * q + 2] * sx * w.z;
+            o[4 * q + 3] = (float)v[4 * q + 3] * sx * w.w;
+          }
+          store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
+        }
+      };
+      for (int c = 0; c < nc; c += 2) {
+        tmem_ld_wait();
+        reg_fence16i(acc[0]);
+        if (c + 1 < nc) tmem_ld16i(tmem + buf * p.tn + lane_off + (c + 1) * 16, acc[1]);
+        emit(c, acc[0]);
+        if (c + 1 < nc) {
+          tmem_ld_wait();
+          reg_fence16i(acc[1]);
+          if (c + 2 < nc) tmem_ld16i(tmem + buf * p.tn + lane_off + (c + 2) * 16, acc[0]);
+          emit(c + 1, acc[1]);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&acc_empty[buf]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, ncols);
+}
+
+// ------------------------------------------------------ weights on the rows
+template <typename TO>
+__global__ void __launch_bounds__(256, 1)
+    k_i8_gemm_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const I8GemmPlan p,
+                  const I8GemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const I8Smem L = i8_layout(p);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L.bar_off);
+  uint64_t* empty = full + p.stages;
+  uint64_t* acc_full = empty + p.stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* s_sx = reinterpret_cast<float*>(smem + L.sw_off);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int f0 = blockIdx.x * 128, split = blockIdx.y, t0 = blockIdx.z * p.tn;
+  const int nkb_all = (a.k + KB - 1) / KB;
+  const int kb0 = (int)((long long)nkb_all * split / p.splits), kb1 = (int)((long long)nkb_all * (split + 1) / p.splits);
+  const int nkb = kb1 - kb0;  // >= 1: the plan has splits <= k blocks
+  const uint32_t ncols = tmem_cols(p.tn);
+  const uint32_t sbytes = stage_bytes(p.tn);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    s_flag[0] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, ncols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_launch_dependents();
+
+  if (warp == 0 && lane == 0) {
+    // the weights of the first ring do not wait for the quantiser
+    const int npre = min(nkb, p.stages);
+    for (int i = 0; i < npre; ++i) {
+      mbar_arrive_expect_tx(&full[i], sbytes);
+      tma_load_2d(smem + (size_t)i * sbytes, &tmW, (kb0 + i) * KB, f0, &full[i]);
+    }
+    pdl_wait();
+    for (int i = 0; i < npre; ++i)
+      tma_load_2d(smem + (size_t)i * sbytes + 128 * KB, &tmX, (kb0 + i) * KB, t0, &full[i]);
+    int it = npre;
+    for (; it < nkb; ++it) {
+      const int st = it % p.stages;
+      if (!mbar_wait(&empty[st], ((it / p.stages) & 1) ^ 1, a.err.wait_ns)) {
+        s_flag[0] = 1;
+        set_error(a.err, DEV_TIMEOUT);
+        break;
+      }
+      uint8_t* s = smem + (size_t)st * sbytes;
+      mbar_arrive_expect_tx(&full[st], sbytes);
+      tma_load_2d(s, &tmW, (kb0 + it) * KB, f0, &full[st]);
+      tma_load_2d(s + 128 * KB, &tmX, (kb0 + it) * KB, t0, &full[st]);
+    }
+    for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
+      if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
+  } else if (warp == 1 && lane == 0) {
+    const uint32_t idesc = idesc_i8(128, p.tn);
+    for (int it = 0; it < nkb; ++it) {
+      const int st = it % p.stages;
+      if (!mbar_wait(&full[st], (it / p.stages) & 1, a.err.wait_ns)) {
+        s_flag[0] = 1;
+        set_error(a.err, DEV_TIMEOUT);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t sa = smem_u32(smem + (size_t)st * sbytes);
+      const uint64_t ad = sw128_desc(sa, 16, 1024), bd = sw128_desc(sa + 128 * KB, 16, 1024);
+#pragma unroll
+      for (int kk = 0; kk < KB / 32; ++kk)
+        umma_i8(tmem, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, (it | kk) != 0 ? 1u : 0u);
+      umma_commit(&empty[st]);
+    }
+    umma_commit(acc_full);  // always issued, so the epilogue's wait ends
+  }
+  __syncwarp();
+  pdl_wait();
+  const bool acc_ok = mbar_wait(acc_full, 0, kDrainNs);
+  if (!acc_ok) set_error(a.err, DEV_DRAIN);
+  tc_fence_after();
+  for (int i = threadIdx.x; i < p.tn; i += 256) s_sx[i] = t0 + i < a.tokens ? a.sx[t0 + i] : 0.f;
+  const bool ok = __syncthreads_and(acc_ok ? 1 : 0) != 0 && s_flag[0] == 0;
+
+  // warp w: TMEM lanes 32 (w % 4).. (features), 16-token chunks c with c % 2 == w / 4
+  const int row = (warp & 3) * 32 + lane;
+  const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  TO* y = static_cast<TO*>(a.y);
+  const int nc = p.tn / 16;
+  const int ntok = min(p.tn, a.tokens - t0);
+  if (p.splits == 1) {
+    const int f = f0 + row;
+    const float sw = f < a.n ? a.sw[f] : 0.f;
+    if (ok)
+      for (int c = warp >> 2; c < nc; c += 2) {
+        int v[16];
+        tmem_ld16i(trow + c * 16, v);
+        tmem_ld_wait();
+        reg_fence16i(v);
+        if (f < a.n) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c * 16 + j < ntok)
+              st_out(y + (size_t)(t0 + c * 16 + j) * a.ldy + f, (float)v[j] * s_sx[c * 16 + j] * sw);
+        }
+      }
+  } else {
+    // partials [token][128 features] in this CTA's shared memory; rank r of the
+    // cluster sums and writes features [r R, r R + R) of every token
+    int* part = reinterpret_cast<int*>(smem + L.part_off);
+    if (ok)
+      for (int c = warp >> 2; c < nc; c += 2) {
+        int v[16];
+        tmem_ld16i(trow + c * 16, v);
+        tmem_ld_wait();
+        reg_fence16i(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c * 16 + j) * 128 + row] = v[j];
+      }
+    cluster_sync();
+    const int S = p.splits, R = 128 / S;
+    const int rank = (int)cluster_rank();
+    if (ok) {
+      for (int e = threadIdx.x; e < R * ntok; e += 256) {
+        const int tok = e / R, r = rank * R + e % R;
+        const uint32_t at = smem_u32(part + tok * 128 + r);
+        int v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < S) v[q] = __float_as_int(ld_cluster_f32(map_cluster(at, (uint32_t)q)));
+        int sum = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (q < S) sum += v[q];
+        const int f = f0 + r;
+        if (f < a.n) st_out(y + (size_t)(t0 + tok) * a.ldy + f, (float)sum * s_sx[tok] * a.sw[f]);
+      }
+    }
+    cluster_sync();  // no rank leaves while another still reads its partials
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, ncols);
+}
+
+}  // namespace
+
+// Tokens go to the N side while they fit one tile of at most 64: the weights
+// are then read once and padding stays under 16 tokens.  With more, tokens on
+// the rows; the N tile is the one whose waves of 148 CTAs cost least, a tile's
+// cost being its operand bytes (shared-memory fills bound the main loop) plus
+// a fixed start and end.
+I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
+  I8GemmPlan p{};
+  const int nkb = (k + KB - 1) / KB;
+  p.splits = 1;
+  if (tokens <= 64) {
+    p.swap = 1;
+    p.tn = std::max(16, (tokens + 15) / 16 * 16);
+    p.tiles_m = (n + 127) / 128;
+    p.tiles_n = 1;
+    while (p.splits < 8 && p.splits * 2 <= nkb && p.tiles_m * p.splits * 2 <= 148) p.splits *= 2;
+    const uint32_t part = p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u;
+    p.stages = std::min({8, (nkb + p.splits - 1) / p.splits, (int)((196u * 1024u - part) / stage_bytes(p.tn))});
+  } else {
+    p.tiles_m = (tokens + 127) / 128;
+    double best = 0;
+    for (int tn = 32; tn <= 256; tn += 16) {
+      if (tn > 32 && tn - 16 >= n) break;
+      const int tiles = p.tiles_m * ((n + tn - 1) / tn);
+      const int waves = (tiles + 147) / 148;
+      const double cost = waves * ((double)nkb * (128 + tn) + 1200.0);
+      if (p.tn == 0 || cost < best * 0.999) {
+        best = cost;
+        p.tn = tn;
+      }
+    }
+    p.tiles_n = (n + p.tn - 1) / p.tn;
+    p.ctas = std::min(148, p.tiles_m * p.tiles_n);
+    p.stages = std::min(8, (int)(196u * 1024u / stage_bytes(p.tn)));
+  }
+  p.stages = std::max(2, p.stages);
+  return p;
+}
+
+cudaError_t i8_gemm_init() {
+  cudaError_t e = cudaSuccess;
+  const int smem = 227 * 1024;
+  auto set = [&](auto kern) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  };
+  set(k_i8_gemm<float>);
+  set(k_i8_gemm<bf16>);
+  set(k_i8_gemm_few<float>);
+  set(k_i8_gemm_few<bf16>);
+  return e;
+}
+
+template <typename TO>
+static cudaError_t i8_launch(const CUtensorMap& r, const CUtensorMap& c, const I8GemmPlan& p, const I8GemmArgs& a,
+                             cudaStream_t st) {
+  const size_t smem = i8_layout(p).total;
+  if (p.swap)
+    return launch_ex(k_i8_gemm_few<TO>, dim3(p.tiles_m, p.splits, p.tiles_n), dim3(256), smem, st, p.splits, false, r,
+                     c, p, a);
+  return launch_ex(k_i8_gemm<TO>, dim3(p.ctas), dim3(256), smem, st, 1, false, r, c, p, a);
+}
+
+cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols, const I8GemmPlan& p,
+                           const I8GemmArgs& a, cudaStream_t st) {
+  return out_bf16 ? i8_launch<bf16>(*tm_rows, *tm_cols, p, a, st) : i8_launch<float>(*tm_rows, *tm_cols, p, a, st);
+}
+
+}  // namespace pae

@@ -338,6 +338,96 @@ pae_status pae_precompute_tables_static(int layers, int width, int dtype, const 
                                         const double* t, int K, float* tables, float* dt,
                                         pae_stream stream);
 
+/* ------------------------------------------------ 8-bit prefix operators
+ * A prefix in 8 bits: rows quantised per token, products of 8-bit integers,
+ * a K/V cache that is quantised as it is written, and attention over it.
+ * These calls need no context and allocate no device memory; pointers are
+ * memory of the current device, work goes to `stream`.  Messages are those of
+ * pae_last_error(NULL).  A device-side bounded wait that runs out (2 s) makes
+ * the next of these calls on the device, or pae_int8_sync, return
+ * PAE_ERR_TIMEOUT until pae_int8_clear_error; after a failed drain (the
+ * message says so) the error stays.  The first call on a device sets up the
+ * kernels and an error word in host memory and cannot be captured into a
+ * graph (PAE_ERR_STATE); pae_int8_init does it ahead.  Later calls can be
+ * captured.  Calls on different streams may overlap, apart from sharing a
+ * workspace, a cache position or an output.  Results are bitwise reproducible.
+ *
+ * A row x in 8 bits: scale s = max|x| / 127 rounded to fp32 (0 if below
+ * 2^-120: the row is stored as zeros), codes rint(x_i / s) of the exact
+ * quotient, ties to even, in [-127, 127]; read back as code * s.  A row that
+ * holds a NaN or an infinity gets scale NaN: it reads back as NaN. */
+pae_status pae_int8_init(void);
+pae_status pae_int8_sync(pae_stream stream);
+void pae_int8_clear_error(void);
+
+/* x [rows][width], row stride ldx >= width elements (PAE_FP32 or PAE_BF16) ->
+ * codes [rows][width] and scale [rows].  rms_eps > 0 quantises the RMSNorm of
+ * each row, x / sqrt(mean(x^2) + rms_eps) (no gain: fold one into the weights
+ * that follow); 0 quantises x itself.  Also lays out weights for
+ * pae_linear_i8, once: rows = output channels. */
+pae_status pae_quantize_rows(const void* x, long long ldx, int rows, int width, int dtype, float rms_eps,
+                             signed char* codes, float* scale, pae_stream stream);
+
+/* y[t][f] = (sum_k x[t][k] w[f][k]) x_scale[t] w_scale[f]: x [tokens][k], w
+ * [n][k] 8-bit codes (16-byte aligned), exact 32-bit sums, y [tokens][n] with
+ * row stride ldy >= n in PAE_FP32 or PAE_BF16 (rounded once).  k a multiple of
+ * 16, at most 131056 (else PAE_ERR_UNSUPPORTED); tokens == 0 is a no-op. */
+pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signed char* w, const float* w_scale,
+                         int tokens, int n, int k, void* y, long long ldy, int dtype, pae_stream stream);
+
+/* An int8 K/V cache in buffers of the caller: codes [n_slots][n_kv_heads]
+ * [capacity][head_dim] (16-byte aligned), one fp32 scale per (slot, head,
+ * position).  head_dim 64, 128 or 256. */
+typedef struct {
+  signed char *k, *v;
+  float *k_scale, *v_scale;
+  int n_slots, n_kv_heads, capacity, head_dim;
+} pae_kv8;
+
+/* Quantise K/V rows into the cache, or read them back.  Packed rows of n_seq
+ * sequences: sequence b (slot b) is rows [cu_rows[b], cu_rows[b + 1]) (device
+ * int32 [n_seq + 1], non-decreasing; NULL: one sequence of all n_rows rows) and its first
+ * row stands at position start[b] (device int32 [n_seq]; NULL: 0).  Row t,
+ * head h is at k + t * k_strides[0] + h * k_strides[1] elements, head_dim of
+ * them contiguous (host arrays; NULL: dense [n_rows][n_kv_heads][head_dim];
+ * rows must start on 16 bytes, so K and V may be slices of one projection).
+ * Write leaves every position that no row goes to as it was; rows outside the
+ * sequences or past the capacity are dropped.  Read fills such rows with
+ * zeros. */
+pae_status pae_kv8_write(const pae_kv8* cache, const void* k, const void* v, const long long* k_strides,
+                         const long long* v_strides, const int* cu_rows, const int* start, int n_seq, int n_rows,
+                         int dtype, pae_stream stream);
+pae_status pae_kv8_read(const pae_kv8* cache, void* k, void* v, const long long* k_strides, const long long* v_strides,
+                        const int* cu_rows, const int* start, int n_seq, int n_rows, int dtype, pae_stream stream);
+
+/* Attention of n_q queries of each of n_seq sequences (slots 0..n_seq-1) over
+ * cached positions [0, lens[b]) (device int32, clamped to [0, capacity]):
+ * query head h reads KV head h / (n_q_heads / n_kv_heads), scores times
+ * `scale` (0: 1 / sqrt(head_dim)).
+ *  - n_new > 0: n_new fresh keys and values per sequence (bf16, not in the
+ *    cache) are visible to every query besides the cached ones (the denoise
+ *    loop's action tokens).
+ *  - causal: the last n_q cached positions are the queries' own; query i sees
+ *    positions [0, lens[b] - n_q + i].  Not together with n_new.
+ * A query that sees no key gives zeros.  q, out and the fresh rows are bf16
+ * with head_dim contiguous elements at strides (sequence, token, head) in
+ * elements, multiples of 8, on 16 bytes.  out may equal q.  workspace:
+ * pae_kv8_workspace bytes (the same sizes; 0 possible), not shared by calls
+ * that may overlap; its contents carry nothing from call to call.
+ * PAE_ERR_UNSUPPORTED: n_seq * n_kv_heads > 65535. */
+typedef struct {
+  const int* lens;
+  const void* q;
+  void* out;
+  const void *k_new, *v_new;
+  long long q_strides[3], out_strides[3], k_new_strides[3], v_new_strides[3];
+  int n_seq, n_q, n_q_heads, n_new, causal;
+  float scale;
+} pae_kv8_query;
+pae_status pae_kv8_workspace(const pae_kv8* cache, int n_seq, int n_q, int n_q_heads, int n_new, size_t* bytes);
+pae_status pae_kv8_attention(const pae_kv8* cache, const pae_kv8_query* q, void* workspace, size_t workspace_bytes,
+                             pae_stream stream);
+
 /* Free everything the context owns.  NULL is a no-op. */
 void pae_destroy(pae_ctx* ctx);
 
