@@ -22,6 +22,7 @@ LIB_PATH = os.path.join(HERE, "libpae.so")
 
 PAE_OK, PAE_ERR_ARG, PAE_ERR_STATE, PAE_ERR_CUDA, PAE_ERR_OOM, PAE_ERR_TIMEOUT, PAE_ERR_UNSUPPORTED = range(7)
 PAE_FP32, PAE_BF16, PAE_W4A16 = 0, 1, 2
+PAE_KV_INT8, PAE_PREFIX_W8A8 = 0x100, 0x200  # dtype flags: the prefix in 8 bits
 PAE_OPT_USE_GRAPH, PAE_OPT_WAIT_LIMIT_US, PAE_OPT_PROFILE, PAE_OPT_PDL, PAE_OPT_MAX_SPLITK = 1, 2, 3, 4, 5
 PAE_OPT_PERSISTENT = 6
 PAE_OPT_FUSED_NORM = 7
@@ -295,13 +296,14 @@ DTYPE_CODES = {"fp32": PAE_FP32, "bf16": PAE_BF16, "w4a16": PAE_W4A16}
 
 def make_config(layers, width, n_q_heads, n_kv_heads, head_dim, mlp_dim, action_dim, chunk,
                 max_batch, max_prefix, dtype, group_size=128, rms_eps=1e-6, rope_base=0.0,
-                prefix_width=0) -> pae_config:
+                prefix_width=0, kv_int8=False, prefix_w8a8=False) -> pae_config:
     c = pae_config()
     for k, v in dict(layers=layers, width=width, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=head_dim,
                      mlp_dim=mlp_dim, action_dim=action_dim, chunk=chunk, max_batch=max_batch,
                      max_prefix=max_prefix, group_size=group_size, prefix_width=prefix_width).items():
         setattr(c, k, int(v))
     c.dtype = DTYPE_CODES[dtype] if isinstance(dtype, str) else int(dtype)
+    c.dtype |= (PAE_KV_INT8 if kv_int8 else 0) | (PAE_PREFIX_W8A8 if prefix_w8a8 else 0)
     c.rms_eps = float(rms_eps)
     c.rope_base = float(rope_base)
     return c

@@ -9,7 +9,8 @@ namespace pae {
 
 // [q | k | v] = y W_qkv^T: q goes to the per-request head-major buffer
 // q[b][hq][i][:], k and v into this layer's KV slot of request b right after its
-// prefix (position lens[b] + i), so attention reads one contiguous key range.
+// prefix (position lens[b] + i), so attention reads one contiguous key range
+// (position i of a buffer of their own when the prefix cache is int8).
 template <typename TA>
 __device__ __forceinline__ void epi_qkv(const Shape& s, const EpiArgs& e, int m, int f, float acc) {
   const int b = m / s.H, i = m - b * s.H;
@@ -22,7 +23,7 @@ __device__ __forceinline__ void epi_qkv(const Shape& s, const EpiArgs& e, int m,
     const bool is_v = f >= qd + kvd;
     const int fk = f - qd - (is_v ? kvd : 0);
     const int g = fk / s.d, j = fk - g * s.d;
-    const int pos = e.lens[b] + i;
+    const int pos = (e.kv_fresh ? 0 : e.lens[b]) + i;
     const size_t off = (((size_t)(e.layer * s.Bmax + b) * s.Hkv + g) * s.Ptot + pos) * s.d + j;
     st_act<TA>(static_cast<TA*>(is_v ? e.vc : e.kc) + off, acc);
   }

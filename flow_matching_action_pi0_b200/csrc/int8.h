@@ -56,7 +56,10 @@ struct Kv8Io {              // row (t, head) at p + t * tok + head * head_stride
   void *k, *v;
   long long k_tok, k_head, v_tok, v_head;
 };
-cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
+// rope_cs (fp32 rows only; null: off): (cos, sin) [position][d / 2]; keys are
+// rotated at their position before they are quantised.
+cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, const float2* rope_cs,
+                             cudaStream_t st);
 cudaError_t launch_kv8_read(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
@@ -84,6 +87,11 @@ struct Kv8AttnArgs {
   float2* part_ml;          // [n_seq * heads][splits][rows] (max in the log2 domain, sum)
   DevErr err;
 };
+// Place the partial rows and their statistics in a workspace of p.ws_bytes.
+inline void kv8_attn_parts(Kv8AttnArgs* a, const Kv8AttnPlan& p, void* workspace) {
+  a->part_o = static_cast<float*>(workspace);
+  a->part_ml = reinterpret_cast<float2*>(a->part_o + p.ws_bytes / ((size_t)a->c.d * 4 + 8) * a->c.d);
+}
 cudaError_t kv8_attn_init();
 cudaError_t launch_kv8_attn(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st);
 

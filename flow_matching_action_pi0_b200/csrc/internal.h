@@ -99,6 +99,9 @@ struct EpiArgs {
   void* u;            // [M][F]
   // rotary embedding (EPI_QKV, EPI_PREFIX keys): (cos, sin) [Ptot][d/2], null = off
   const float2* rope_cs;
+  // EPI_QKV: 1 = the action keys go to positions [0, H) of a buffer of their own
+  // (int8 prefix cache) instead of behind the prefix
+  int kv_fresh;
   // EPI_PREFIX: token m is prefix position m of request `prefix_row`; keys and
   // values go to kc / vc of `layer`
   int prefix_row;

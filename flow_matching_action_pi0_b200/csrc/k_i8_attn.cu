@@ -377,7 +377,7 @@ cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cud
                    1, pdl, a);
 }
 template <int D>
-cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {
+cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {  // (PDL behind its own attention)
   return launch_ex(k_kv8_merge<D>, dim3(a.group * a.n_q, a.n_seq * a.c.heads), dim3(256), 0, st, 1, true, a, p.splits,
                    p.qtiles * (p.tc ? 128 : 8));
 }

@@ -79,6 +79,10 @@ struct Vec8<float> {
     b = reinterpret_cast<const uint4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void put(const float* f) {
+    a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+  }
   __device__ __forceinline__ uint32_t amax() const {
     const uint32_t k = 0x7FFFFFFFu;
     return max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)), max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
@@ -270,8 +274,9 @@ __device__ __forceinline__ bool kv8_place(const Kv8Rows& r, int cap, int t, int&
 
 // d / 8 lanes per row; a thread takes UNR (token, head) pairs, K and V of each
 // loaded before any is quantised.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) k_kv8_write(const Kv8 c, const Kv8Rows r, const Kv8Io io, long long items) {
+template <typename T, int D, bool ROPE>
+__global__ void __launch_bounds__(256)
+    k_kv8_write(const Kv8 c, const Kv8Rows r, const Kv8Io io, const float2* __restrict__ rope_cs, long long items) {
   constexpr int LPR = D / 8, UNR = 2;
   const int sub = threadIdx.x % LPR;
   const long long gstep = (long long)gridDim.x * (256 / LPR);
@@ -300,6 +305,21 @@ __global__ void __launch_bounds__(256) k_kv8_write(const Kv8 c, const Kv8Rows r,
       int slot = 0, pos = 0;
       const bool ok = it[u] < items && kv8_place(r, c.cap, tok[u], slot, pos);
       const size_t row = ((size_t)slot * c.heads + (ok ? head[u] : 0)) * c.cap + pos;
+      if constexpr (ROPE) {
+        // Rotate-half: channel i < d/2 pairs with i + d/2, which the lane LPR/2
+        // away holds: a' = a cos - b sin, b' = b cos + a sin.
+        float f[8], g[8];
+        kv[u][0].get(f);
+        const bool hi = sub >= LPR / 2;
+        const float2* cs = rope_cs + (size_t)(ok ? pos : 0) * (D / 2) + (sub % (LPR / 2)) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float o = __shfl_xor_sync(0xFFFFFFFFu, f[i], LPR / 2);
+          const float2 t = cs[i];
+          g[i] = hi ? f[i] * t.x + o * t.y : f[i] * t.x - o * t.y;
+        }
+        kv[u][0].put(g);
+      }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         uint32_t am = kv[u][w].amax();
@@ -371,16 +391,16 @@ int kv8_grid(long long items, int d, int unr) {
   return (int)std::min<long long>((items + per - 1) / per, 148 * 8);
 }
 
-template <typename T>
-cudaError_t kv8_write_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st) {
+template <typename T, bool ROPE>
+cudaError_t kv8_write_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, const float2* cs, cudaStream_t st) {
   const long long items = (long long)r.n_rows * c.heads;
   const int grid = kv8_grid(items, c.d, 2);
   if (c.d == 64)
-    k_kv8_write<T, 64><<<grid, 256, 0, st>>>(c, r, io, items);
+    k_kv8_write<T, 64, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
   else if (c.d == 128)
-    k_kv8_write<T, 128><<<grid, 256, 0, st>>>(c, r, io, items);
+    k_kv8_write<T, 128, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
   else
-    k_kv8_write<T, 256><<<grid, 256, 0, st>>>(c, r, io, items);
+    k_kv8_write<T, 256, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
   return cudaGetLastError();
 }
 
@@ -405,8 +425,10 @@ cudaError_t launch_quantize_rows(bool in_bf16, const void* x, long long ldx, int
                  : quant_sel<float>(x, ldx, rows, width, rms_eps, codes, scale, st);
 }
 
-cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st) {
-  return bf16_rows ? kv8_write_sel<bf16>(c, r, io, st) : kv8_write_sel<float>(c, r, io, st);
+cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, const float2* rope_cs,
+                             cudaStream_t st) {
+  if (bf16_rows) return rope_cs ? cudaErrorInvalidValue : kv8_write_sel<bf16, false>(c, r, io, nullptr, st);
+  return rope_cs ? kv8_write_sel<float, true>(c, r, io, rope_cs, st) : kv8_write_sel<float, false>(c, r, io, nullptr, st);
 }
 
 cudaError_t launch_kv8_read(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st) {

@@ -112,7 +112,7 @@ __device__ __forceinline__ bf16* rot_head_base(const Shape& s, const EpiArgs& e,
     pos = len + t;
     if (head < s.Hq) return static_cast<bf16*>(e.q) + ((size_t)(b * s.Hq + head) * s.H + t) * s.d;
     return static_cast<bf16*>(e.kc) +
-           (((size_t)(e.layer * s.Bmax + b) * s.Hkv + (head - s.Hq)) * s.Ptot + len + t) * s.d;
+           (((size_t)(e.layer * s.Bmax + b) * s.Hkv + (head - s.Hq)) * s.Ptot + (e.kv_fresh ? 0 : len) + t) * s.d;
   }
 }
 
@@ -175,7 +175,8 @@ __device__ __forceinline__ void epi_vec16(const Shape& s, const EpiArgs& e, int 
       const bool is_v = f >= qd + kvd;
       const int fk = f - qd - (is_v ? kvd : 0);
       const int g = fk / s.d, j = fk - g * s.d;
-      const size_t off = (((size_t)(e.layer * s.Bmax + b) * s.Hkv + g) * s.Ptot + e.lens[b] + t) * s.d + j;
+      const size_t off =
+          (((size_t)(e.layer * s.Bmax + b) * s.Hkv + g) * s.Ptot + (e.kv_fresh ? 0 : e.lens[b]) + t) * s.d + j;
       store16_bf16(static_cast<bf16*>(is_v ? e.vc : e.kc) + off, v);
     }
   }
@@ -267,7 +268,7 @@ __device__ __forceinline__ void epi_vec4(const Shape& s, const EpiArgs& e, int m
       const int fk = f - qd - (is_v ? kvd : 0);
       const int g = fk / s.d, j = fk - g * s.d;
       dst = static_cast<bf16*>(is_v ? e.vc : e.kc) +
-            (((size_t)(e.layer * s.Bmax + b) * s.Hkv + g) * s.Ptot + len + t) * s.d + j;
+            (((size_t)(e.layer * s.Bmax + b) * s.Hkv + g) * s.Ptot + (e.kv_fresh ? 0 : len) + t) * s.d + j;
     }
     store4_bf16(dst, a0.x, a0.y, a0.z, a0.w);
   }

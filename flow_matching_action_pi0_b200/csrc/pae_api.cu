@@ -22,6 +22,7 @@
 #include "pae.h"
 #include "internal.h"
 #include "epilogue.cuh"
+#include "int8.h"
 
 using namespace pae;
 
@@ -39,6 +40,9 @@ void set_create_error(const char* msg) { g_create_error = msg ? msg : ""; }
 namespace {
 
 constexpr int kMaxSteps = 64;
+// dtype = a pae_dtype, or-ed with the 8-bit prefix flags
+constexpr int kPrefixFlags = PAE_KV_INT8 | PAE_PREFIX_W8A8;
+int base_dtype(const pae_config* c) { return c->dtype & ~kPrefixFlags; }
 constexpr int kSsSlots = 256;  // sum-of-squares slots: (D / 128) tiles x split-K ranks
 constexpr int kDefaultMaxSplitK = 8;  // PAE_OPT_MAX_SPLITK until set
 
@@ -55,6 +59,7 @@ struct Plan {
   int B = 0, M = 0;
   TcPlan qkv{}, o{}, gu{}, down{};
   AttnPlan attn{};
+  Kv8AttnPlan attn8{};  // int8 prefix cache
   bool persist = false;  // eligible for the persistent kernel
   PersistArgs pa{};
   bool flow = false;       // eligible for the dataflow loop (clusters, per-tile counters)
@@ -186,6 +191,18 @@ struct pae_ctx {
   void* w_pkv = nullptr;
   void* ypre = nullptr;
   CUtensorMap tmWpkv{}, tmYpre{};
+  // int8 prefix cache (PAE_KV_INT8): codes and scales [L][Bmax][Hkv][Pmax][d];
+  // kc / vc then hold the action keys alone ([L][Bmax][Hkv][H][d], shape
+  // s_fresh).  Prefix production goes through one slot of bf16 rows
+  // (shape s_scratch) or, with PAE_PREFIX_W8A8, through int8 products.
+  int kv8 = 0, w8a8 = 0;
+  Shape s_fresh{}, s_scratch{};
+  Kv8 cache8{};
+  void* kv8_ws = nullptr;                          // split-KV partial rows
+  void *scr_k = nullptr, *scr_v = nullptr;         // [Hkv][Pmax][d]
+  int8_t *w8 = nullptr, *x8 = nullptr;             // [L][2 Hkv d][Dp] weights, [Pmax][Dp] hidden states
+  float *w8_scale = nullptr, *x8_scale = nullptr;
+  float* y8 = nullptr;                             // [Pmax][2 Hkv d]
   // prefix slots
   void *kc = nullptr, *vc = nullptr;
   int* lens_dev = nullptr;
@@ -273,6 +290,31 @@ pae_status make_map(pae_ctx* ctx, CUtensorMap* m, const void* base, uint64_t inn
     return fail(ctx, PAE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for [%llu][%llu] box %ux%u", (int)r,
                 (unsigned long long)outer, (unsigned long long)inner, box_outer, box_inner);
   return PAE_OK;
+}
+
+pae_status make_map_i8(pae_ctx* ctx, CUtensorMap* m, const void* base, uint64_t k, uint64_t rows, uint32_t box_rows) {
+  // int8 codes [rows][k], 128-byte swizzled boxes of box_rows x 128.
+  cuuint64_t dims[2] = {k, rows};
+  cuuint64_t strides[1] = {k};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  CUresult r = ctx->encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(ctx, PAE_ERR_CUDA, "cuTensorMapEncodeTiled (int8) failed (%d)", (int)r);
+  return PAE_OK;
+}
+
+// The cache of one layer.
+Kv8 layer_cache8(const pae_ctx* ctx, int layer) {
+  const Shape& s = ctx->s;
+  Kv8 c = ctx->cache8;
+  const size_t rows = (size_t)layer * s.Bmax * s.Hkv * c.cap;
+  c.k += rows * s.d;
+  c.v += rows * s.d;
+  c.k_scale += rows;
+  c.v_scale += rows;
+  return c;
 }
 
 pae_status make_map_f32(pae_ctx* ctx, CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
@@ -457,7 +499,7 @@ AttnPlan plan_attn(const Shape& s, int B) {
 bool plan_persistent(const pae_ctx* ctx, int B, PersistArgs* pa) {
   const Shape& s = ctx->s;
   const int M = B * s.H, n = ctx->ncta;
-  if (!ctx->act_bf16 || ctx->w4 || s.rope || n < 1 || M > 64 || M > n) return false;
+  if (!ctx->act_bf16 || ctx->w4 || ctx->kv8 || s.rope || n < 1 || M > 64 || M > n) return false;
   if (s.d != 64 && s.d != 128 && s.d != 256) return false;
   if ((size_t)(s.D + s.A) * 4 > 128 * 1024) return false;
   *pa = PersistArgs{};
@@ -525,7 +567,7 @@ bool plan_persistent(const pae_ctx* ctx, int B, PersistArgs* pa) {
 bool plan_flow(const pae_ctx* ctx, int B, FlowArgs* fa) {
   const Shape& s = ctx->s;
   const int M = B * s.H;
-  if (!ctx->flow_capable || M < 1 || M > 64) return false;
+  if (!ctx->flow_capable || ctx->kv8 || M < 1 || M > 64) return false;
   if (s.D % 128 || s.D > 1024 || s.qkv_rows % 128 || s.F % 128 || s.attn_dim % 64) return false;
   const int nkD = s.D / 64, nkA = s.attn_dim / 64, nkF = s.F / 64;
   const int qtiles = (s.G * s.H + 127) / 128;
@@ -660,6 +702,7 @@ pae_status build_plan(pae_ctx* ctx, int B, Plan* P) {
     return fail(ctx, PAE_ERR_UNSUPPORTED, "split-KV plan exceeds the merge scratch (%d splits)", P->attn.splits);
   P->fuse_norm = LP.fuse_norm;
   P->factored = LP.factored;
+  if (ctx->kv8) P->attn8 = plan_kv8_attn(B, s.Hkv, s.G, s.H, s.H, s.Pmax, s.d);
   const uint64_t Mmax = (uint64_t)s.Bmax * s.H;
   pae_status st;
   if ((st = make_map(ctx, &P->tmY, ctx->y, s.D, Mmax, 64, P->qkv.tn)) != PAE_OK) return st;
@@ -784,7 +827,38 @@ void run_gemm(pae_ctx* ctx, const Plan& P, int which, int layer, const EpiArgs& 
     a.nscale = norm.scale;
     a.nshift = norm.shift;
   }
-  note_launch(ctx, launch_tc_gemm(s, tw, tx, na, *p, a, pdl_on(ctx), st));
+  // the QKV epilogue of an int8 prefix cache scatters k / v with the action keys' own strides
+  note_launch(ctx, launch_tc_gemm(which == 0 && ctx->kv8 ? ctx->s_fresh : s, tw, tx, na, *p, a, pdl_on(ctx), st));
+}
+
+// Attention of layer l over the int8 prefix cache and this step's action keys.
+void run_attention8(pae_ctx* ctx, const Plan& P, int l, cudaStream_t st) {
+  const Shape& s = ctx->s;
+  Kv8AttnArgs a{};
+  a.c = layer_cache8(ctx, l);
+  a.lens = ctx->lens_dev;
+  a.q = static_cast<const bf16*>(ctx->q);
+  a.q_seq = (long long)s.Hq * s.H * s.d;
+  a.q_tok = s.d;
+  a.q_head = (long long)s.H * s.d;
+  a.o = static_cast<bf16*>(ctx->o);
+  a.o_seq = (long long)s.H * s.attn_dim;
+  a.o_tok = s.attn_dim;
+  a.o_head = s.d;
+  const size_t fresh = (size_t)l * s.Bmax * s.Hkv * s.H * s.d;
+  a.k_new = static_cast<const bf16*>(ctx->kc) + fresh;
+  a.v_new = static_cast<const bf16*>(ctx->vc) + fresh;
+  a.kn_seq = a.vn_seq = (long long)s.Hkv * s.H * s.d;
+  a.kn_tok = a.vn_tok = s.d;
+  a.kn_head = a.vn_head = (long long)s.H * s.d;
+  a.n_seq = P.B;
+  a.n_q = s.H;
+  a.n_new = s.H;
+  a.group = s.G;
+  a.scale_log2 = 1.4426950408889634f / std::sqrt((float)s.d);
+  kv8_attn_parts(&a, P.attn8, ctx->kv8_ws);
+  a.err = DevErr{ctx->err_dev, ctx->wait_ns};
+  note_launch(ctx, launch_kv8_attn(P.attn8, a, pdl_on(ctx), st));
 }
 
 // Enqueue Euler steps k_begin..k_end-1 for the plan's batch on `st`, with the
@@ -830,6 +904,7 @@ void enqueue_steps(pae_ctx* ctx, const Plan& P, int k_begin, int k_end, cudaStre
       e.vc = ctx->vc;
       e.lens = ctx->lens_dev;
       e.rope_cs = ctx->rope_cs;
+      e.kv_fresh = ctx->kv8;
       if (P.factored) {
         e.f_bias = ctx->bias_qkv + ((size_t)k * s.L + l) * s.qkv_rows;
         e.f_ss = ctx->ss_buf;
@@ -844,7 +919,9 @@ void enqueue_steps(pae_ctx* ctx, const Plan& P, int k_begin, int k_end, cudaStre
       }
       {
         ProfScope ps(ctx, PAE_K_ATTENTION, st);
-        if (ctx->act_bf16) {
+        if (ctx->kv8) {
+          run_attention8(ctx, P, l, st);
+        } else if (ctx->act_bf16) {
           AttnArgs aa{};
           aa.lens = ctx->lens_dev;
           aa.layer = l;
@@ -1099,8 +1176,15 @@ pae_status validate_config(const pae_config* c) {
       !is_pos(c->head_dim) || !is_pos(c->mlp_dim) || !is_pos(c->action_dim) || !is_pos(c->chunk) ||
       !is_pos(c->max_batch) || c->max_prefix < 0 || !(c->rms_eps > 0.f))
     return fail(nullptr, PAE_ERR_ARG, "config: sizes must be positive (max_prefix >= 0, rms_eps > 0)");
-  if (c->dtype != PAE_FP32 && c->dtype != PAE_BF16 && c->dtype != PAE_W4A16)
+  const int dtype = base_dtype(c), flags = c->dtype & kPrefixFlags;
+  if (dtype != PAE_FP32 && dtype != PAE_BF16 && dtype != PAE_W4A16)
     return fail(nullptr, PAE_ERR_ARG, "config: unknown dtype %d", c->dtype);
+  if (flags && dtype == PAE_FP32)
+    return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: the 8-bit prefix needs PAE_BF16 or PAE_W4A16");
+  if ((flags & PAE_PREFIX_W8A8) && (!(flags & PAE_KV_INT8) || c->prefix_width <= 0))
+    return fail(nullptr, PAE_ERR_ARG, "config: PAE_PREFIX_W8A8 needs PAE_KV_INT8 and prefix_width > 0");
+  if (flags && (long long)c->max_batch * c->n_kv_heads > 65535)
+    return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: the 8-bit prefix needs max_batch * n_kv_heads <= 65535");
   if (c->n_q_heads % c->n_kv_heads != 0)
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: n_q_heads must be a multiple of n_kv_heads");
   if (c->n_q_heads / c->n_kv_heads > 16)
@@ -1112,13 +1196,13 @@ pae_status validate_config(const pae_config* c) {
   if (c->rope_base > 0.f && c->head_dim % 2 != 0)
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: rotary embedding needs an even head_dim");
   if (c->prefix_width < 0) return fail(nullptr, PAE_ERR_ARG, "config: prefix_width must be >= 0");
-  if (c->prefix_width > 0 && c->dtype != PAE_FP32 &&
+  if (c->prefix_width > 0 && dtype != PAE_FP32 &&
       (c->prefix_width % 64 != 0 || (2 * c->n_kv_heads * c->head_dim) % 128 != 0))
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: bf16 prefix production needs prefix_width % 64 == 0 and "
                                               "2*n_kv_heads*head_dim % 128 == 0");
-  if (c->dtype == PAE_W4A16 && c->group_size != 128)
+  if (dtype == PAE_W4A16 && c->group_size != 128)
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: W4A16 needs group_size 128");
-  if (c->dtype != PAE_FP32) {
+  if (dtype != PAE_FP32) {
     const int qd = c->n_q_heads * c->head_dim;
     if (c->width % 128 || qd % 128 || c->mlp_dim % 128 || (c->n_kv_heads * c->head_dim) % 64)
       return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: bf16 kernels need width, n_q_heads*head_dim, mlp_dim "
@@ -1163,7 +1247,7 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
   for (int l = 0; l < cfg->layers; ++l)
     if (!w->w_qkv[l] || !w->w_o[l] || !w->w_gate[l] || !w->w_up[l] || !w->w_down[l])
       return fail(nullptr, PAE_ERR_ARG, "layer %d weight pointer is NULL", l);
-  if (cfg->dtype == PAE_W4A16) {
+  if (base_dtype(cfg) == PAE_W4A16) {
     if (!w->s_qkv || !w->s_o || !w->s_gate || !w->s_up || !w->s_down)
       return fail(nullptr, PAE_ERR_ARG, "W4A16 needs the s_* scale arrays");
     for (int l = 0; l < cfg->layers; ++l)
@@ -1175,8 +1259,14 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
   ctx->cfg = *cfg;
   ctx->s = shape_from_config(cfg);
   Shape& s = ctx->s;
-  ctx->act_bf16 = cfg->dtype != PAE_FP32;
-  ctx->w4 = cfg->dtype == PAE_W4A16;
+  ctx->act_bf16 = base_dtype(cfg) != PAE_FP32;
+  ctx->w4 = base_dtype(cfg) == PAE_W4A16;
+  ctx->kv8 = (cfg->dtype & PAE_KV_INT8) != 0;
+  ctx->w8a8 = (cfg->dtype & PAE_PREFIX_W8A8) != 0;
+  ctx->s_fresh = ctx->s_scratch = s;
+  ctx->s_fresh.Ptot = s.H;
+  ctx->s_scratch.Bmax = 1;
+  ctx->s_scratch.Ptot = std::max(s.Pmax, 1);
   ctx->esize = ctx->act_bf16 ? 2 : 4;
   const size_t es = ctx->esize;
   ctx->lens_host.assign(s.Bmax, -1);
@@ -1213,6 +1303,8 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
     }
     ctx->encode = reinterpret_cast<EncodeTiledFn>(fn);
     CKC(tc_gemm_init());
+    if (ctx->kv8) CKC(kv8_attn_init());
+    if (ctx->w8a8) CKC(i8_gemm_init());
   }
   CKC(cudaStreamCreateWithFlags(&ctx->cap_stream, cudaStreamNonBlocking));
   CKC(cudaHostAlloc(reinterpret_cast<void**>(&ctx->err_host), sizeof(int), cudaHostAllocMapped));
@@ -1334,11 +1426,30 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
   ALLOC(ctx->cbuf, sizeof(float) * kMaxSteps * D);
   ALLOC(ctx->tables, sizeof(float) * kMaxSteps * (size_t)s.table_rows);
   ALLOC(ctx->dt, sizeof(float) * kMaxSteps);
-  const size_t slot_elems = (size_t)L * s.Bmax * s.Hkv * s.Ptot * s.d;
+  const size_t slot_elems = (size_t)L * s.Bmax * s.Hkv * (ctx->kv8 ? s.H : s.Ptot) * s.d;
   ALLOC(ctx->kc, slot_elems * es);
   ALLOC(ctx->vc, slot_elems * es);
   CKC(cudaMemsetAsync(ctx->kc, 0, slot_elems * es, cs));
   CKC(cudaMemsetAsync(ctx->vc, 0, slot_elems * es, cs));
+  if (ctx->kv8) {
+    Kv8& c = ctx->cache8;
+    c.slots = s.Bmax;
+    c.heads = s.Hkv;
+    c.cap = std::max(s.Pmax, 1);
+    c.d = s.d;
+    const size_t rows = (size_t)L * s.Bmax * s.Hkv * c.cap;
+    ALLOC(c.k, rows * s.d);
+    ALLOC(c.v, rows * s.d);
+    ALLOC(c.k_scale, rows * sizeof(float));
+    ALLOC(c.v_scale, rows * sizeof(float));
+    CKC(cudaMemsetAsync(c.k, 0, rows * s.d, cs));
+    CKC(cudaMemsetAsync(c.v, 0, rows * s.d, cs));
+    CKC(cudaMemsetAsync(c.k_scale, 0, rows * sizeof(float), cs));
+    CKC(cudaMemsetAsync(c.v_scale, 0, rows * sizeof(float), cs));
+    size_t ws = 0;
+    for (int B = 1; B <= s.Bmax; ++B) ws = std::max(ws, plan_kv8_attn(B, s.Hkv, s.G, s.H, s.H, s.Pmax, s.d).ws_bytes);
+    ALLOC(ctx->kv8_ws, ws);
+  }
   if (s.rope) {
     // (cos, sin) per position and channel pair, angles in float64 from the
     // integer positions, each rounded once to fp32
@@ -1355,19 +1466,38 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
   }
   if (s.Dp > 0) {
     const int kvr = 2 * s.Hkv * s.d;
-    ALLOC(ctx->w_pkv, (size_t)L * kvr * s.Dp * es);
-    ALLOC(ctx->ypre, (size_t)std::max(s.Pmax, 1) * s.Dp * es);
+    const size_t pm = (size_t)std::max(s.Pmax, 1);
+    if (ctx->w8a8) {
+      ALLOC(ctx->w8, (size_t)L * kvr * s.Dp);
+      ALLOC(ctx->w8_scale, (size_t)L * kvr * sizeof(float));
+      ALLOC(ctx->x8, pm * s.Dp);
+      ALLOC(ctx->x8_scale, pm * sizeof(float));
+      ALLOC(ctx->y8, pm * kvr * sizeof(float));
+    } else {
+      ALLOC(ctx->w_pkv, (size_t)L * kvr * s.Dp * es);
+      ALLOC(ctx->ypre, pm * s.Dp * es);
+      if (ctx->kv8) {
+        ALLOC(ctx->scr_k, pm * s.Hkv * s.d * es);
+        ALLOC(ctx->scr_v, pm * s.Hkv * s.d * es);
+      }
+    }
     for (int l = 0; l < L; ++l) {
       if (!w->w_prefix_kv || !w->w_prefix_kv[l]) {
         fail(ctx, PAE_ERR_ARG, "prefix_width > 0 needs w_prefix_kv for every layer");
         return bail(PAE_ERR_ARG);
+      }
+      if (ctx->w8a8) {
+        // one scale per output channel, rows in their natural order (the cache's write rotates the keys)
+        CKC(launch_quantize_rows(true, w->w_prefix_kv[l], s.Dp, kvr, s.Dp, 0.f, ctx->w8 + (size_t)l * kvr * s.Dp,
+                                 ctx->w8_scale + (size_t)l * kvr, cs));
+        continue;
       }
       k_permute_rows<<<256, 256, 0, cs>>>((const uint16_t*)w->w_prefix_kv[l],
                                           (uint16_t*)((char*)ctx->w_pkv + (size_t)l * kvr * s.Dp * es), kvr,
                                           (int)(s.Dp * es / 2), s.rope ? s.Hkv * s.d : 0, s.d);
       CKC(cudaGetLastError());
     }
-    if (ctx->act_bf16) {
+    if (ctx->act_bf16 && !ctx->w8a8) {
       if ((st = make_map(ctx, &ctx->tmWpkv, ctx->w_pkv, s.Dp, (uint64_t)L * kvr, 64, 128)) != PAE_OK) return bail(st);
       if ((st = make_map(ctx, &ctx->tmYpre, ctx->ypre, s.Dp, (uint64_t)std::max(s.Pmax, 1), 64, 128)) != PAE_OK)
         return bail(st);
@@ -1448,7 +1578,7 @@ pae_status pae_create(const pae_config* cfg, const pae_weights* w, pae_ctx** out
   }
   if (ctx->act_bf16) {
     CKC(attn_tc_init());
-    const uint64_t kv_rows = (uint64_t)L * s.Bmax * s.Hkv * s.Ptot;
+    const uint64_t kv_rows = (uint64_t)L * s.Bmax * s.Hkv * (ctx->kv8 ? s.H : s.Ptot);
     if ((st = make_map(ctx, &ctx->tmQ, ctx->q, s.d, (uint64_t)s.Bmax * s.Hq * s.H, 64, 128)) != PAE_OK) return bail(st);
     if ((st = make_map(ctx, &ctx->tmK, ctx->kc, s.d, kv_rows, 64, 64)) != PAE_OK) return bail(st);
     if ((st = make_map(ctx, &ctx->tmV, ctx->vc, s.d, kv_rows, 64, 64)) != PAE_OK) return bail(st);
@@ -1477,7 +1607,18 @@ pae_status pae_set_prefix(pae_ctx* ctx, int row, const void* const* k_per_layer,
   cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
   const size_t es = ctx->esize;
   const size_t rowb = (size_t)s.d * es;
+  if (ctx->kv8)
+    for (int l = 0; l < s.L && len > 0; ++l)
+      if (((uintptr_t)k_per_layer[l] | (uintptr_t)v_per_layer[l]) & 15)
+        return fail(ctx, PAE_ERR_ARG, "layer %d: K/V rows must start on 16 bytes to be quantised", l);
   for (int l = 0; l < s.L && len > 0; ++l) {
+    if (ctx->kv8) {
+      const long long tok = (long long)s.Hkv * s.d;
+      CK(launch_kv8_write(true, layer_cache8(ctx, l), Kv8Rows{nullptr, nullptr, 1, len, row},
+                          Kv8Io{const_cast<void*>(k_per_layer[l]), const_cast<void*>(v_per_layer[l]), tok, s.d, tok, s.d},
+                          nullptr, stm));
+      continue;
+    }
     for (int g = 0; g < s.Hkv; ++g) {
       const size_t slot = (((size_t)l * s.Bmax + row) * s.Hkv + g) * s.Ptot * s.d * es;
       const char* ks = static_cast<const char*>(k_per_layer[l]) + g * rowb;
@@ -1489,6 +1630,29 @@ pae_status pae_set_prefix(pae_ctx* ctx, int row, const void* const* k_per_layer,
   k_set_len<<<1, 1, 0, stm>>>(ctx->lens_dev, row, len);
   CK(cudaGetLastError());
   ctx->lens_host[row] = len;
+  return PAE_OK;
+}
+
+// Prefix production with int8 products: per layer, the hidden states' RMSNorm
+// in 8 bits per token, the key and value rows by the int8 product (fp32 out),
+// then rotation of the keys and quantisation into the row's slot.
+static pae_status produce_prefix_w8a8(pae_ctx* ctx, int row, const void* const* h_per_layer, int len, cudaStream_t stm) {
+  const Shape& s = ctx->s;
+  const int kvr = 2 * s.Hkv * s.d;
+  const I8GemmPlan p = plan_i8_gemm(len, kvr, s.Dp);
+  CUtensorMap tx, tw;
+  pae_status st = make_map_i8(ctx, &tx, ctx->x8, s.Dp, len, p.swap ? p.tn : 128);
+  if (st != PAE_OK) return st;
+  const I8GemmArgs base{ctx->x8_scale, nullptr, ctx->y8, kvr, len, kvr, s.Dp, DevErr{ctx->err_dev, ctx->wait_ns}};
+  for (int l = 0; l < s.L; ++l) {
+    if ((st = make_map_i8(ctx, &tw, ctx->w8 + (size_t)l * kvr * s.Dp, s.Dp, kvr, p.swap ? 128 : p.tn)) != PAE_OK) return st;
+    CK(launch_quantize_rows(true, h_per_layer[l], s.Dp, len, s.Dp, s.eps, ctx->x8, ctx->x8_scale, stm));
+    I8GemmArgs a = base;
+    a.sw = ctx->w8_scale + (size_t)l * kvr;
+    CK(launch_i8_gemm(false, p.swap ? &tw : &tx, p.swap ? &tx : &tw, p, a, stm));
+    CK(launch_kv8_write(false, layer_cache8(ctx, l), Kv8Rows{nullptr, nullptr, 1, len, row},
+                        Kv8Io{ctx->y8, ctx->y8 + s.Hkv * s.d, kvr, s.d, kvr, s.d}, ctx->rope_cs, stm));
+  }
   return PAE_OK;
 }
 
@@ -1509,7 +1673,10 @@ pae_status pae_set_prefix_hidden(pae_ctx* ctx, int row, const void* const* h_per
   cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
   const int kvr = 2 * s.Hkv * s.d;
   const TcPlan plan = ctx->act_bf16 && len > 0 ? prefix_plan(s, len) : TcPlan{};
-  for (int l = 0; l < s.L && len > 0; ++l) {
+  if (ctx->w8a8 && len > 0) {
+    if ((st = produce_prefix_w8a8(ctx, row, h_per_layer, len, stm)) != PAE_OK) return st;
+  }
+  for (int l = 0; l < s.L && len > 0 && !ctx->w8a8; ++l) {
     CK(launch_prefix_norm(ctx->act_bf16, h_per_layer[l], ctx->ypre, len, s.Dp, s.eps, stm));
     EpiArgs e{};
     e.epi = EPI_PREFIX;
@@ -1519,6 +1686,12 @@ pae_status pae_set_prefix_hidden(pae_ctx* ctx, int row, const void* const* h_per
     e.layer = l;
     e.prefix_row = row;
     e.rope_cs = ctx->rope_cs;
+    if (ctx->kv8) {  // bf16 rows into the scratch slot, quantised from there
+      e.kc = ctx->scr_k;
+      e.vc = ctx->scr_v;
+      e.layer = 0;
+      e.prefix_row = 0;
+    }
     if (!ctx->act_bf16) {
       launch_gemm_simple(s, static_cast<const float*>(ctx->ypre),
                          static_cast<const float*>(ctx->w_pkv) + (size_t)l * kvr * s.Dp, kvr, s.Dp, e, stm);
@@ -1529,7 +1702,12 @@ pae_status pae_set_prefix_hidden(pae_ctx* ctx, int row, const void* const* h_per
       a.K = s.Dp;
       a.w_row0 = l * kvr;
       a.err = DevErr{ctx->err_dev, ctx->wait_ns};
-      CK(launch_tc_gemm(s, &ctx->tmWpkv, &ctx->tmYpre, 1, plan, a, false, stm));
+      CK(launch_tc_gemm(ctx->kv8 ? ctx->s_scratch : s, &ctx->tmWpkv, &ctx->tmYpre, 1, plan, a, false, stm));
+      if (ctx->kv8) {
+        const long long head = (long long)ctx->s_scratch.Ptot * s.d;
+        CK(launch_kv8_write(true, layer_cache8(ctx, l), Kv8Rows{nullptr, nullptr, 1, len, row},
+                            Kv8Io{ctx->scr_k, ctx->scr_v, s.d, head, s.d, head}, nullptr, stm));
+      }
     }
     CK(cudaGetLastError());
   }
@@ -1723,11 +1901,11 @@ pae_status pae_query(pae_ctx* ctx, int what, int batch, long long* value) {
                ((long long)P->down.splits << 24);
       return PAE_OK;
     case PAE_Q_TOKEN_TILE: *value = P->qkv.tn; return PAE_OK;
-    case PAE_Q_ATTN_SPLITS: *value = P->attn.splits; return PAE_OK;
+    case PAE_Q_ATTN_SPLITS: *value = ctx->kv8 ? P->attn8.splits : P->attn.splits; return PAE_OK;
     case PAE_Q_PERSISTENT: *value = use_persist(ctx, P) ? 1 : 0; return PAE_OK;
     case PAE_Q_FUSED_NORM: *value = P->fuse_norm ? 1 : P->factored ? 2 : 0; return PAE_OK;
     case PAE_Q_DATAFLOW: *value = use_flow(ctx, P) ? P->fa.C : 0; return PAE_OK;
-    case PAE_Q_ATTN_CHUNK: *value = ctx->act_bf16 ? P->attn.chunk : 0; return PAE_OK;
+    case PAE_Q_ATTN_CHUNK: *value = ctx->kv8 ? 64 : ctx->act_bf16 ? P->attn.chunk : 0; return PAE_OK;
     default: return fail(ctx, PAE_ERR_ARG, "unknown query %d", what);
   }
 }
@@ -1741,17 +1919,19 @@ pae_status pae_plan_query(const pae_config* cfg, int what, int batch, long long*
       what != PAE_Q_ATTN_CHUNK)
     return fail(nullptr, PAE_ERR_ARG, "query %d needs a context", what);
   *value = 0;
-  if (cfg->dtype == PAE_FP32) return PAE_OK;  // CUDA-core kernels: no tensor-core launch plan
+  if (base_dtype(cfg) == PAE_FP32) return PAE_OK;  // CUDA-core kernels: no tensor-core launch plan
   const Shape s = shape_from_config(cfg);
-  const LaunchPlans L = plan_launches(s, batch, cfg->dtype == PAE_W4A16, kDefaultMaxSplitK, false, false);
+  const LaunchPlans L = plan_launches(s, batch, base_dtype(cfg) == PAE_W4A16, kDefaultMaxSplitK, false, false);
   switch (what) {
     case PAE_Q_SPLITS:
       *value = (long long)L.qkv.splits | ((long long)L.o.splits << 8) | ((long long)L.gu.splits << 16) |
                ((long long)L.down.splits << 24);
       break;
     case PAE_Q_TOKEN_TILE: *value = L.qkv.tn; break;
-    case PAE_Q_ATTN_SPLITS: *value = L.attn.splits; break;
-    case PAE_Q_ATTN_CHUNK: *value = L.attn.chunk; break;
+    case PAE_Q_ATTN_SPLITS:
+      *value = (cfg->dtype & PAE_KV_INT8) ? plan_kv8_attn(batch, s.Hkv, s.G, s.H, s.H, s.Pmax, s.d).splits : L.attn.splits;
+      break;
+    case PAE_Q_ATTN_CHUNK: *value = (cfg->dtype & PAE_KV_INT8) ? 64 : L.attn.chunk; break;
     default: *value = L.fuse_norm ? 1 : L.factored ? 2 : 0; break;
   }
   return PAE_OK;
@@ -1790,8 +1970,12 @@ pae_status pae_debug_copy(pae_ctx* ctx, const char* name, void* dst_host, size_t
   else if (nm == "q") { src = ctx->q; n = Mmax * s.attn_dim * es; }
   else if (nm == "o") { src = ctx->o; n = Mmax * s.attn_dim * es; }
   else if (nm == "u") { src = ctx->u; n = Mmax * s.F * es; }
-  else if (nm == "kcache") { src = ctx->kc; n = (size_t)s.L * s.Bmax * s.Hkv * s.Ptot * s.d * es; }
-  else if (nm == "vcache") { src = ctx->vc; n = (size_t)s.L * s.Bmax * s.Hkv * s.Ptot * s.d * es; }
+  else if (nm == "kcache") { src = ctx->kc; n = (size_t)s.L * s.Bmax * s.Hkv * (ctx->kv8 ? s.H : s.Ptot) * s.d * es; }
+  else if (nm == "vcache") { src = ctx->vc; n = (size_t)s.L * s.Bmax * s.Hkv * (ctx->kv8 ? s.H : s.Ptot) * s.d * es; }
+  else if (ctx->kv8 && nm == "kcodes") { src = ctx->cache8.k; n = (size_t)s.L * s.Bmax * s.Hkv * ctx->cache8.cap * s.d; }
+  else if (ctx->kv8 && nm == "vcodes") { src = ctx->cache8.v; n = (size_t)s.L * s.Bmax * s.Hkv * ctx->cache8.cap * s.d; }
+  else if (ctx->kv8 && nm == "kscales") { src = ctx->cache8.k_scale; n = sizeof(float) * (size_t)s.L * s.Bmax * s.Hkv * ctx->cache8.cap; }
+  else if (ctx->kv8 && nm == "vscales") { src = ctx->cache8.v_scale; n = sizeof(float) * (size_t)s.L * s.Bmax * s.Hkv * ctx->cache8.cap; }
   else if (nm == "tables") { src = ctx->tables; n = sizeof(float) * (size_t)std::max(ctx->K, 1) * s.table_rows; }
   else if (nm == "dt") { src = ctx->dt; n = sizeof(float) * std::max(ctx->K, 1); }
   else if (nm == "lens") { src = ctx->lens_dev; n = sizeof(int) * s.Bmax; }

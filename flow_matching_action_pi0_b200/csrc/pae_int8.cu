@@ -161,7 +161,7 @@ pae_status kv8_io(const char* fn, bool write, const pae_kv8* cache, void* k, voi
   const Kv8Rows r{cu, start, n_seq, n_rows, 0};
   const Kv8Io io{k, v, ks[0], ks[1], vs[0], vs[1]};
   cudaStream_t sm = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = write ? launch_kv8_write(dtype == PAE_BF16, view(cache), r, io, sm)
+  const cudaError_t e = write ? launch_kv8_write(dtype == PAE_BF16, view(cache), r, io, nullptr, sm)
                               : launch_kv8_read(dtype == PAE_BF16, view(cache), r, io, sm);
   return e == cudaSuccess ? PAE_OK : cuda_fail(fn, e);
 }
@@ -338,10 +338,7 @@ pae_status pae_kv8_attention(const pae_kv8* cache, const pae_kv8_query* q, void*
   a.group = q->n_q_heads / cache->n_kv_heads;
   a.causal = q->causal != 0;
   a.scale_log2 = (q->scale == 0.f ? 1.f / std::sqrt((float)cache->head_dim) : q->scale) * 1.4426950408889634f;
-  a.part_o = static_cast<float*>(workspace);
-  // partial rows first, then their statistics
-  const size_t rows = p.ws_bytes / ((size_t)cache->head_dim * 4 + 8);
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + rows * cache->head_dim);
+  kv8_attn_parts(&a, p, workspace);
   a.err = DevErr{d->err_dev, kWaitNs};
   const cudaError_t e = launch_kv8_attn(p, a, false, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PAE_OK : cuda_fail(fn, e);

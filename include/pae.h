@@ -57,6 +57,19 @@ typedef enum {
   PAE_W4A16 = 2   /* int4 projection weights (group-wise bf16 scales), bf16 inputs  */
 } pae_dtype;
 
+/* Flags for pae_config.dtype, or-ed with PAE_BF16 or PAE_W4A16: the prefix in
+ * 8 bits (rows and scales as in the 8-bit prefix operators below).
+ * PAE_KV_INT8: prefix K/V are quantised as pae_set_prefix and
+ *   pae_set_prefix_hidden write them (one scale per token and KV head), half
+ *   the bytes of the bf16 slots; every Euler step attends over them and the
+ *   action tokens' own bf16 keys.  K/V rows given to pae_set_prefix must start
+ *   on 16 bytes.  PAE_OPT_PERSISTENT and PAE_OPT_DATAFLOW run the graph.
+ * PAE_PREFIX_W8A8 (with PAE_KV_INT8 and prefix_width > 0):
+ *   pae_set_prefix_hidden projects in 8-bit integers; w_prefix_kv is quantised
+ *   at pae_create with one scale per output row, the normalised hidden states
+ *   with one per token. */
+enum { PAE_KV_INT8 = 0x100, PAE_PREFIX_W8A8 = 0x200 };
+
 /*
  * Model shape.  L = layers, D = width, Hq/Hkv = query/KV heads, d = head_dim,
  * F = mlp_dim, A = action_dim, H = chunk (action tokens per request).
@@ -84,7 +97,7 @@ typedef enum {
 typedef struct {
   int layers, width, n_q_heads, n_kv_heads, head_dim, mlp_dim, action_dim, chunk;
   int max_batch, max_prefix, group_size;
-  int dtype;        /* pae_dtype */
+  int dtype;        /* pae_dtype, or-ed with PAE_KV_INT8, PAE_PREFIX_W8A8 */
   float rms_eps;
   float rope_base;  /* 0: off */
   int prefix_width; /* 0: no pae_set_prefix_hidden */
@@ -305,7 +318,9 @@ const char* pae_last_error(const pae_ctx* ctx);
 
 /* Copy an internal buffer to host memory for inspection (synchronous).
  * name: "x", "h", "y", "q", "o", "u", "kcache", "vcache", "tables", "dt",
- * "lens".  *bytes in: capacity of dst; out: bytes of the buffer (dst may be
+ * "lens"; with PAE_KV_INT8 "kcache" / "vcache" hold the action keys alone
+ * ([L][max_batch][Hkv][H][d]) and the prefix is "kcodes", "vcodes" (int8
+ * [L][max_batch][Hkv][max(max_prefix, 1)][d]), "kscales", "vscales" (fp32).  *bytes in: capacity of dst; out: bytes of the buffer (dst may be
  * NULL to query the size). */
 pae_status pae_debug_copy(pae_ctx* ctx, const char* name, void* dst_host, size_t* bytes);
 
