@@ -24,6 +24,7 @@ struct I8GemmPlan {
   int swap;     // 1: weight rows on the MMA's M side, tokens on its N side
   int tn;       // N tile (multiple of 16, 16..256)
   int tiles_m, tiles_n;
+  int th;       // swap: weight rows per tile (32, 64 or 128; the MMA always spans 128)
   int splits;   // split-K cluster size (swap only)
   int stages;
   int ctas;     // persistent grid (swap == 0)
@@ -35,6 +36,7 @@ struct I8GemmArgs {
   void* y;
   long long ldy;
   int tokens, n, k;
+  int w_ready;  // 1: no kernel of the stream still writes the weights, so they may be read before the previous one ends
   DevErr err;
 };
 cudaError_t i8_gemm_init();

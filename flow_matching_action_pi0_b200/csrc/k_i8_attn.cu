@@ -35,7 +35,7 @@ namespace pae {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kTileKeys = 16;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -73,7 +73,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 1 : 2) k_kv8_attn_few(const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(const Kv8AttnArgs a) {
   constexpr int KBLK = D / 64;               // 64-channel blocks of a K row
   constexpr int VB = D >= 128 ? 16 : 8;      // bytes of a V row per lane and block
   constexpr int VBLK = D / (8 * VB);         // blocks of a V row

@@ -12,8 +12,10 @@
 //                        accumulator is double-buffered in TMEM, so the
 //                        epilogue of a tile runs under the next one's MMAs
 //   weights on the rows  (few tokens: streaming the weights is what bounds
-//                        it) tokens pad only to a multiple of 16; the k range
-//                        of a tile is split over a cluster of CTAs so that all
+//                        it) tokens pad only to a multiple of 16; tiles of 32
+//                        to 128 weight rows spread the weights over the SMs,
+//                        and where those are too few the k range of a tile is
+//                        split over a cluster of CTAs so that all
 //                        SMs stream weights, and the int32 partials are summed
 //                        through distributed shared memory
 // Warp 0 streams both operands by TMA in 128-byte k blocks (128-byte swizzle)
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(256, 1)
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sx = reinterpret_cast<float*>(smem + L.sw_off);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int f0 = blockIdx.x * 128, split = blockIdx.y, t0 = blockIdx.z * p.tn;
+  const int f0 = blockIdx.x * p.th, split = blockIdx.y, t0 = blockIdx.z * p.tn;
   const int nkb_all = (a.k + KB - 1) / KB;
   const int kb0 = (int)((long long)nkb_all * split / p.splits), kb1 = (int)((long long)nkb_all * (split + 1) / p.splits);
   const int nkb = kb1 - kb0;  // >= 1: the plan has splits <= k blocks
@@ -330,10 +332,13 @@ __global__ void __launch_bounds__(256, 1)
   pdl_launch_dependents();
 
   if (warp == 0 && lane == 0) {
-    // the weights of the first ring do not wait for the quantiser
+    // Tiles of th < 128 weight rows fill the front of the A tile; the MMA's
+    // remaining rows multiply whatever lies behind and are never read.
+    const uint32_t tx = (uint32_t)(p.th + p.tn) * KB;
+    if (!a.w_ready) pdl_wait();
     const int npre = min(nkb, p.stages);
     for (int i = 0; i < npre; ++i) {
-      mbar_arrive_expect_tx(&full[i], sbytes);
+      mbar_arrive_expect_tx(&full[i], tx);
       tma_load_2d(smem + (size_t)i * sbytes, &tmW, (kb0 + i) * KB, f0, &full[i]);
     }
     pdl_wait();
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(256, 1)
         break;
       }
       uint8_t* s = smem + (size_t)st * sbytes;
-      mbar_arrive_expect_tx(&full[st], sbytes);
+      mbar_arrive_expect_tx(&full[st], tx);
       tma_load_2d(s, &tmW, (kb0 + it) * KB, f0, &full[st]);
       tma_load_2d(s + 128 * KB, &tmX, (kb0 + it) * KB, t0, &full[st]);
     }
@@ -387,10 +392,11 @@ __global__ void __launch_bounds__(256, 1)
   TO* y = static_cast<TO*>(a.y);
   const int nc = p.tn / 16;
   const int ntok = min(p.tn, a.tokens - t0);
+  const bool mine = (warp & 3) * 32 < p.th;  // this warp's rows exist
   if (p.splits == 1) {
     const int f = f0 + row;
-    const float sw = f < a.n ? a.sw[f] : 0.f;
-    if (ok)
+    const float sw = mine && f < a.n ? a.sw[f] : 0.f;
+    if (ok && mine)
       for (int c = warp >> 2; c < nc; c += 2) {
         int v[16];
         tmem_ld16i(trow + c * 16, v);
@@ -407,7 +413,7 @@ __global__ void __launch_bounds__(256, 1)
     // partials [token][128 features] in this CTA's shared memory; rank r of the
     // cluster sums and writes features [r R, r R + R) of every token
     int* part = reinterpret_cast<int*>(smem + L.part_off);
-    if (ok)
+    if (ok && mine)
       for (int c = warp >> 2; c < nc; c += 2) {
         int v[16];
         tmem_ld16i(trow + c * 16, v);
@@ -417,22 +423,31 @@ __global__ void __launch_bounds__(256, 1)
         for (int j = 0; j < 16; ++j) part[(c * 16 + j) * 128 + row] = v[j];
       }
     cluster_sync();
-    const int S = p.splits, R = 128 / S;
+    const int S = p.splits, R4 = p.th / S / 4;  // R / 4: groups of 4 features
     const int rank = (int)cluster_rank();
     if (ok) {
-      for (int e = threadIdx.x; e < R * ntok; e += 256) {
-        const int tok = e / R, r = rank * R + e % R;
+      for (int e = threadIdx.x; e < R4 * ntok; e += 256) {
+        const int tok = e / R4, r = (rank * R4 + e % R4) * 4;
         const uint32_t at = smem_u32(part + tok * 128 + r);
-        int v[8];
+        uint4 v[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (q < S) v[q] = __float_as_int(ld_cluster_f32(map_cluster(at, (uint32_t)q)));
-        int sum = 0;
+          if (q < S) v[q] = ld_cluster_u32x4(map_cluster(at, (uint32_t)q));
+        uint4 sum = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (q < S) sum += v[q];
+          if (q < S) {
+            sum.x += v[q].x;
+            sum.y += v[q].y;
+            sum.z += v[q].z;
+            sum.w += v[q].w;
+          }
         const int f = f0 + r;
-        if (f < a.n) st_out(y + (size_t)(t0 + tok) * a.ldy + f, (float)sum * s_sx[tok] * a.sw[f]);
+        const int s4[4] = {(int)sum.x, (int)sum.y, (int)sum.z, (int)sum.w};
+        TO* yp = y + (size_t)(t0 + tok) * a.ldy + f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (f + i < a.n) st_out(yp + i, (float)s4[i] * s_sx[tok] * a.sw[f + i]);
       }
     }
     cluster_sync();  // no rank leaves while another still reads its partials
@@ -456,7 +471,10 @@ I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
   if (tokens <= 64) {
     p.swap = 1;
     p.tn = std::max(16, (tokens + 15) / 16 * 16);
-    p.tiles_m = (n + 127) / 128;
+    // narrower tiles until they occupy most SMs, then split k
+    p.th = 128;
+    while (p.th > 32 && (n + p.th - 1) / p.th < 100) p.th /= 2;
+    p.tiles_m = (n + p.th - 1) / p.th;
     p.tiles_n = 1;
     while (p.splits < 8 && p.splits * 2 <= nkb && p.tiles_m * p.splits * 2 <= 148) p.splits *= 2;
     const uint32_t part = p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u;
@@ -500,9 +518,9 @@ static cudaError_t i8_launch(const CUtensorMap& r, const CUtensorMap& c, const I
                              cudaStream_t st) {
   const size_t smem = i8_layout(p).total;
   if (p.swap)
-    return launch_ex(k_i8_gemm_few<TO>, dim3(p.tiles_m, p.splits, p.tiles_n), dim3(256), smem, st, p.splits, false, r,
+    return launch_ex(k_i8_gemm_few<TO>, dim3(p.tiles_m, p.splits, p.tiles_n), dim3(256), smem, st, p.splits, true, r,
                      c, p, a);
-  return launch_ex(k_i8_gemm<TO>, dim3(p.ctas), dim3(256), smem, st, 1, false, r, c, p, a);
+  return launch_ex(k_i8_gemm<TO>, dim3(p.ctas), dim3(256), smem, st, 1, true, r, c, p, a);
 }
 
 cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols, const I8GemmPlan& p,

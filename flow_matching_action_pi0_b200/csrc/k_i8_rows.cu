@@ -11,7 +11,9 @@
 //
 // Bound: bytes.  Each row is read once into registers (16-byte loads), its
 // maximum found by a shuffle tree over the lanes that share it, and its codes
-// written from the same registers.
+// written from the same registers.  Every kernel here is launched with
+// programmatic dependent launch and waits for its predecessor before it reads
+// anything, so only its start overlaps the predecessor's end.
 #include <algorithm>
 
 #include "int8.h"
@@ -119,6 +121,8 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
                                                        float* __restrict__ scale) {
   __shared__ uint32_t s_max[8];
   __shared__ float s_sum[8];
+  pdl_launch_dependents();
+  pdl_wait();
   constexpr int RPB = 256 / TPR;
   const int lane = threadIdx.x % TPR;
   const int row = blockIdx.x * RPB + threadIdx.x / TPR;
@@ -185,6 +189,8 @@ __global__ void __launch_bounds__(256) k_quantize_rows_any(const T* __restrict__
                                                            float* __restrict__ scale) {
   __shared__ uint32_t s_max[8];
   __shared__ float s_sum[8];
+  pdl_launch_dependents();
+  pdl_wait();
   const int row = blockIdx.x;
   const T* xr = x + (size_t)row * ldx;
   uint32_t am = 0;
@@ -217,9 +223,8 @@ template <typename T, int TPR, int NV>
 cudaError_t quant_launch(const void* x, long long ldx, int rows, int width, float eps, int8_t* codes, float* scale,
                          cudaStream_t st) {
   constexpr int RPB = 256 / TPR;
-  k_quantize_rows<T, TPR, NV><<<(rows + RPB - 1) / RPB, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, width, eps,
-                                                                      codes, scale);
-  return cudaGetLastError();
+  return launch_ex(k_quantize_rows<T, TPR, NV>, dim3((rows + RPB - 1) / RPB), dim3(256), 0, st, 1, true,
+                   static_cast<const T*>(x), ldx, rows, width, eps, codes, scale);
 }
 
 template <typename T>
@@ -228,10 +233,9 @@ cudaError_t quant_sel(const void* x, long long ldx, int rows, int width, float e
   const bool vec = width % 8 == 0 && (reinterpret_cast<uintptr_t>(x) & 15) == 0 &&
                    (ldx * (long long)sizeof(T)) % 16 == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
   const int nv = width / 8;
-  if (!vec || nv > 256 * 8) {
-    k_quantize_rows_any<T><<<rows, 256, 0, st>>>(static_cast<const T*>(x), ldx, rows, width, eps, codes, scale);
-    return cudaGetLastError();
-  }
+  if (!vec || nv > 256 * 8)
+    return launch_ex(k_quantize_rows_any<T>, dim3(rows), dim3(256), 0, st, 1, true, static_cast<const T*>(x), ldx, rows,
+                     width, eps, codes, scale);
   // A warp per row while its registers hold the row; a block per row when the
   // row is longer, or when so few rows would leave most SMs idle.
   constexpr int kWarpNv = sizeof(T) == 2 ? 8 : 4;
@@ -278,6 +282,8 @@ template <typename T, int D, bool ROPE>
 __global__ void __launch_bounds__(256)
     k_kv8_write(const Kv8 c, const Kv8Rows r, const Kv8Io io, const float2* __restrict__ rope_cs, long long items) {
   constexpr int LPR = D / 8, UNR = 2;
+  pdl_launch_dependents();
+  pdl_wait();
   const int sub = threadIdx.x % LPR;
   const long long gstep = (long long)gridDim.x * (256 / LPR);
   const long long g0 = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
@@ -366,6 +372,8 @@ __device__ __forceinline__ void put8<bf16>(bf16* p, const uint2 q, float s) {
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_kv8_read(const Kv8 c, const Kv8Rows r, const Kv8Io io, long long items) {
   constexpr int LPR = D / 8;
+  pdl_launch_dependents();
+  pdl_wait();
   const int sub = threadIdx.x % LPR;
   const long long gstep = (long long)gridDim.x * (256 / LPR);
   for (long long it = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR; it < items; it += gstep) {
@@ -395,26 +403,16 @@ template <typename T, bool ROPE>
 cudaError_t kv8_write_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, const float2* cs, cudaStream_t st) {
   const long long items = (long long)r.n_rows * c.heads;
   const int grid = kv8_grid(items, c.d, 2);
-  if (c.d == 64)
-    k_kv8_write<T, 64, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
-  else if (c.d == 128)
-    k_kv8_write<T, 128, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
-  else
-    k_kv8_write<T, 256, ROPE><<<grid, 256, 0, st>>>(c, r, io, cs, items);
-  return cudaGetLastError();
+  auto kern = c.d == 64 ? k_kv8_write<T, 64, ROPE> : c.d == 128 ? k_kv8_write<T, 128, ROPE> : k_kv8_write<T, 256, ROPE>;
+  return launch_ex(kern, dim3(grid), dim3(256), 0, st, 1, true, c, r, io, cs, items);
 }
 
 template <typename T>
 cudaError_t kv8_read_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st) {
   const long long items = (long long)r.n_rows * c.heads;
   const int grid = kv8_grid(items, c.d, 1);
-  if (c.d == 64)
-    k_kv8_read<T, 64><<<grid, 256, 0, st>>>(c, r, io, items);
-  else if (c.d == 128)
-    k_kv8_read<T, 128><<<grid, 256, 0, st>>>(c, r, io, items);
-  else
-    k_kv8_read<T, 256><<<grid, 256, 0, st>>>(c, r, io, items);
-  return cudaGetLastError();
+  auto kern = c.d == 64 ? k_kv8_read<T, 64> : c.d == 128 ? k_kv8_read<T, 128> : k_kv8_read<T, 256>;
+  return launch_ex(kern, dim3(grid), dim3(256), 0, st, 1, true, c, r, io, items);
 }
 
 }  // namespace

@@ -1643,9 +1643,9 @@ static pae_status produce_prefix_w8a8(pae_ctx* ctx, int row, const void* const* 
   CUtensorMap tx, tw;
   pae_status st = make_map_i8(ctx, &tx, ctx->x8, s.Dp, len, p.swap ? p.tn : 128);
   if (st != PAE_OK) return st;
-  const I8GemmArgs base{ctx->x8_scale, nullptr, ctx->y8, kvr, len, kvr, s.Dp, DevErr{ctx->err_dev, ctx->wait_ns}};
+  const I8GemmArgs base{ctx->x8_scale, nullptr, ctx->y8, kvr, len, kvr, s.Dp, 1, DevErr{ctx->err_dev, ctx->wait_ns}};
   for (int l = 0; l < s.L; ++l) {
-    if ((st = make_map_i8(ctx, &tw, ctx->w8 + (size_t)l * kvr * s.Dp, s.Dp, kvr, p.swap ? 128 : p.tn)) != PAE_OK) return st;
+    if ((st = make_map_i8(ctx, &tw, ctx->w8 + (size_t)l * kvr * s.Dp, s.Dp, kvr, p.swap ? p.th : p.tn)) != PAE_OK) return st;
     CK(launch_quantize_rows(true, h_per_layer[l], s.Dp, len, s.Dp, s.eps, ctx->x8, ctx->x8_scale, stm));
     I8GemmArgs a = base;
     a.sw = ctx->w8_scale + (size_t)l * kvr;

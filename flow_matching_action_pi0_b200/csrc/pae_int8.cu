@@ -249,13 +249,13 @@ pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signe
   const I8GemmPlan p = plan_i8_gemm(tokens, n, k);
   CUtensorMap rows, cols;
   if (p.swap) {
-    if ((st = make_map(d, &rows, w, n, k, 128)) != PAE_OK) return st;
+    if ((st = make_map(d, &rows, w, n, k, p.th)) != PAE_OK) return st;
     if ((st = make_map(d, &cols, x, tokens, k, p.tn)) != PAE_OK) return st;
   } else {
     if ((st = make_map(d, &rows, x, tokens, k, 128)) != PAE_OK) return st;
     if ((st = make_map(d, &cols, w, n, k, p.tn)) != PAE_OK) return st;
   }
-  const I8GemmArgs a{x_scale, w_scale, y, ldy, tokens, n, k, DevErr{d->err_dev, kWaitNs}};
+  const I8GemmArgs a{x_scale, w_scale, y, ldy, tokens, n, k, 0, DevErr{d->err_dev, kWaitNs}};
   const cudaError_t e = launch_i8_gemm(dtype == PAE_BF16, &rows, &cols, p, a, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PAE_OK : cuda_fail(fn, e);
 }
@@ -340,7 +340,7 @@ pae_status pae_kv8_attention(const pae_kv8* cache, const pae_kv8_query* q, void*
   a.scale_log2 = (q->scale == 0.f ? 1.f / std::sqrt((float)cache->head_dim) : q->scale) * 1.4426950408889634f;
   kv8_attn_parts(&a, p, workspace);
   a.err = DevErr{d->err_dev, kWaitNs};
-  const cudaError_t e = launch_kv8_attn(p, a, false, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv8_attn(p, a, true, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PAE_OK : cuda_fail(fn, e);
 }
 
