@@ -65,11 +65,12 @@ cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, con
 cudaError_t launch_kv8_read(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
-constexpr int kMaxKv8Splits = 128;
+constexpr int kMaxKv8Splits = 8;
 struct Kv8AttnPlan {
   int tc;        // 1: tcgen05 tiles of 128 query rows; 0: groups of 8 rows
   int qtiles;    // row tiles (tc) or row groups per (sequence, KV head)
-  int splits;    // key splits; > 1: partial rows go to the workspace and are merged by a second launch
+  int splits;    // tc: key splits; > 1: partial rows go to the workspace and are merged by a second launch
+                 // not tc: blocks that share the keys of all sequences; ws_bytes > 0: merged likewise
   size_t ws_bytes;
 };
 Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new, int max_keys, int d);
@@ -85,8 +86,8 @@ struct Kv8AttnArgs {
   int n_seq, n_q, n_new, group;  // group = query heads per KV head
   int causal;
   float scale_log2;         // softmax scale x log2(e)
-  float* part_o;            // [n_seq * heads][splits][rows][d] unnormalised rows
-  float2* part_ml;          // [n_seq * heads][splits][rows] (max in the log2 domain, sum)
+  float* part_o;            // unnormalised rows: tc [n_seq * heads][splits][rows][d], else [blocks][2][8][d]
+  float2* part_ml;          // their (max in the log2 domain, sum)
   DevErr err;
 };
 // Place the partial rows and their statistics in a workspace of p.ws_bytes.

@@ -22,9 +22,16 @@
 //   V: lane (g, t) loads 16 channels [128 h + 16 g, +16) of keys 2t, 2t + 1,
 //      2t + 8, 2t + 9; product m of block h takes channels 2 m (row g) and
 //      2 m + 1 (row g + 8)
-// Each warp of the block takes every W-th group of 16 keys with statistics of
-// its own; the warps meet once at the end.  Long caches and small batches
-// split the keys over blocks (partials in fp32, merged by k_kv8_merge).
+// Work is cut into units of 64 keys (16 per warp) of one (sequence, KV head,
+// row group); every sequence has one at least.  Units in that order are dealt
+// out evenly: block i of G takes units [T i / G, T (i + 1) / G), whatever the
+// lengths, so a batch of ragged sequences finishes together (an equal number
+// of splits per sequence left the SMs to the longest ones: 36.8 us for 48
+// sequences of up to 8192 keys).  Inside a block each warp has statistics of
+// its own and the warps meet once per sequence.  A sequence that lies in one
+// block is written out by it; of the others each block parks its fp32 rows in
+// one of its two workspace slots (0: the part continues an earlier block's, 1:
+// it begins here), and k_kv8_merge_few joins them.
 #include <algorithm>
 #include <cmath>
 
@@ -69,32 +76,98 @@ __device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return (uint32_t)__bfloat16_as_ushort(f2bf(lo)) | ((uint32_t)__bfloat16_as_ushort(f2bf(hi)) << 16);
+  uint32_t r;  // one instruction for the pair, round to nearest even
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Units of 64 keys of a sequence: at least one, so that an empty sequence is
+// written (as zeros) by some block.
+constexpr int kUnit = kWarps * kTileKeys;
+__device__ __forceinline__ int seq_len(const Kv8AttnArgs& a, int b) { return max(0, min(__ldg(a.lens + b), a.c.cap)); }
+__device__ __forceinline__ int seq_units(int len) { return len < 1 ? 1 : (len - 1) / kUnit + 1; }
+
+// Exclusive prefix sums of the sequences' units over the block: thread i holds
+// a slice [b0, b1) and gets the units before it; returns the total.  `sh` has
+// NT / 32 entries.
+template <int NT>
+__device__ __forceinline__ long long scan_units(const Kv8AttnArgs& a, long long* sh, int& b0, int& b1, long long& before) {
+  const int per = (a.n_seq + NT - 1) / NT, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  b0 = min(a.n_seq, (int)threadIdx.x * per);
+  b1 = min(a.n_seq, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += seq_units(seq_len(a, b));
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  __syncthreads();
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  long long total = 0, pre = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) pre += sh[w];
+    total += sh[w];
+  }
+  before = pre + inc - mine;
+  return total;
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(const Kv8AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(const Kv8AttnArgs a, int rgs) {
   constexpr int KBLK = D / 64;               // 64-channel blocks of a K row
   constexpr int VB = D >= 128 ? 16 : 8;      // bytes of a V row per lane and block
   constexpr int VBLK = D / (8 * VB);         // blocks of a V row
   constexpr int VM = VB / 2;                 // products per block
+  constexpr int STEP = kUnit;
   extern __shared__ float s_o[];             // [kWarps][8][D + 4]
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+  __shared__ float2 s_row[8];
+  __shared__ long long s_scan[kWarps];
+  __shared__ int s_b;
+  __shared__ long long s_before;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int split = blockIdx.x, splits = gridDim.x, rg = blockIdx.y, bg = blockIdx.z;
-  const int b = bg / a.c.heads, h = bg - b * a.c.heads;
   const int rows = a.group * a.n_q;
+  const int hr = a.c.heads * rgs;  // items (KV head, row group) of a sequence
   pdl_launch_dependents();
   pdl_wait();
 
-  const int len = max(0, min(a.lens[b], a.c.cap));
-  // this block's keys: an equal share of those any of its rows can see, in
-  // whole groups of kWarps tiles
-  constexpr int STEP = kWarps * kTileKeys;
-  const int share = (int)((((long long)len + splits - 1) / splits + STEP - 1) / STEP) * STEP;
-  const long long k_lo = (long long)split * share;
-  const int key0 = (int)min((long long)len, k_lo), key1 = (int)min((long long)len, k_lo + share);
+  // this block's units, and the sequence the first of them lies in
+  long long unit, unit_end;
+  int b;
+  long long b_unit;  // first unit of sequence b
+  {
+    int b0, b1;
+    long long before;
+    const long long total = scan_units<kWarps * 32>(a, s_scan, b0, b1, before) * hr;
+    const long long G = min((long long)gridDim.x, total);  // blocks with units
+    if (blockIdx.x >= G) return;
+    unit = total * blockIdx.x / G;
+    unit_end = total * (blockIdx.x + 1) / G;
+    before *= hr;
+    for (int i = b0; i < b1; ++i) {
+      const long long n = (long long)seq_units(seq_len(a, i)) * hr;
+      if (before <= unit && unit < before + n) {
+        s_b = i;
+        s_before = before;
+      }
+      before += n;
+    }
+    __syncthreads();
+    b = s_b;
+    b_unit = s_before;
+  }
+
+  while (unit < unit_end) {
+  const int len = seq_len(a, b), units = seq_units(len);
+  const int item = (int)((unit - b_unit) / units), u0 = (int)((unit - b_unit) - (long long)item * units);
+  const int u1 = (int)min((long long)units, u0 + (unit_end - unit));
+  const int h = item / rgs, rg = item - h * rgs;
+  const int key0 = min(len, u0 * STEP), key1 = (int)min((long long)len, (long long)u1 * STEP);
 
   // Q: row r = query * group + head-in-group; lane (g, t) holds channels
   // [64 j + 16 t, +16) of row 8 rg + g
@@ -281,15 +354,22 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
         *reinterpret_cast<float4*>(dst + (8 * VB) * j + VB * g + 2 * m) =
             make_float4(o[j][m][i] * f, o[j][m][2 + i] * f, o[j][m + 1][i] * f, o[j][m + 1][2 + i] * f);
   }
-  __syncthreads();
-  const int rowsp = gridDim.y * 8;
-  for (int e = threadIdx.x; e < 8 * (D / 4); e += kWarps * 32) {
-    const int r = e / (D / 4), c4 = e - r * (D / 4);
+  // a row's statistics, by one warp's first lanes
+  if (threadIdx.x < 8) {
+    const int r = threadIdx.x;
     float M = -INFINITY, l = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) l += s_m[w][r] == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - M);
+    s_row[r] = make_float2(M, l);
+  }
+  __syncthreads();
+  const bool whole = u0 == 0 && u1 == units;
+#pragma unroll
+  for (int e = threadIdx.x; e < 8 * (D / 4); e += kWarps * 32) {
+    const int r = e / (D / 4), c4 = e - r * (D / 4);
+    const float M = s_row[r].x, l = s_row[r].y;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -300,7 +380,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       acc.w += x.w;
     }
     const int row = rg * 8 + r;
-    if (splits == 1) {
+    if (whole) {
       if (row < rows) {
         const int qi = row / a.group, hl = row - qi * a.group;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
@@ -308,15 +388,104 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
         *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
       }
     } else {
-      const size_t pr = ((size_t)bg * splits + split) * rowsp + row;
-      if (M != -INFINITY) *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = acc;
+      const size_t pr = ((size_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * 8 + r;
+      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = acc;
       if (c4 == 0) a.part_ml[pr] = make_float2(M, l);
     }
   }
+  unit += u1 - u0;
+  if (unit - b_unit == (long long)units * hr) {  // on to the next sequence
+    b_unit = unit;
+    ++b;
+  }
+  __syncthreads();  // s_o and the statistics are free again
+  }
 }
 
-// o = sum_s w_s O_s / sum_s w_s l_s with w_s = 2^(m_s - max m): one block per
-// (sequence, KV head, row).  Splits without a visible key (m = -inf) wrote no
+// Joins the parts of the (sequence, KV head, row group) items that
+// k_kv8_attn_few left to several blocks: one block per (row, item).
+template <int D>
+__global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int rgs, int blocks) {
+  constexpr int C4 = D / 4, NS = 256 / C4;
+  __shared__ long long s_scan[8];
+  __shared__ long long s_before;
+  __shared__ float s_red[32];
+  __shared__ float4 s_acc[256];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int item_all = blockIdx.x, r = blockIdx.y;  // ((sequence, KV head), row group); row of the group
+  const int hr = a.c.heads * rgs, b = item_all / hr, item = item_all - b * hr;
+  const int h = item / rgs, rg = item - h * rgs;
+  const int row = rg * 8 + r;
+  if (row >= a.group * a.n_q) return;
+  const int units = seq_units(seq_len(a, b));
+  long long total;
+  {
+    int b0, b1;
+    long long before;
+    total = scan_units<256>(a, s_scan, b0, b1, before) * hr;
+    for (int i = b0; i < b1; ++i) {
+      if (i == b) s_before = before;
+      before += seq_units(seq_len(a, i));
+    }
+    __syncthreads();
+  }
+  const long long first = s_before * hr + (long long)item * units, last = first + units - 1;
+  // block i of G holds units [total i / G, total (i + 1) / G)
+  const long long G = min((long long)blocks, total);
+  const int c0 = (int)(((first + 1) * G - 1) / total), c1 = (int)(((last + 1) * G - 1) / total);
+  if (c0 == c1) return;  // written by its one block
+  const int tid = threadIdx.x;
+  auto slot = [&](int c) -> size_t {  // the item begins in c0 only
+    return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 8 + r;
+  };
+  float M = -INFINITY;
+  for (int c = c0 + tid; c <= c1; c += 256) M = fmaxf(M, __ldcg(&a.part_ml[slot(c)].x));
+  M = warp_max(M);
+  if ((tid & 31) == 0) s_red[tid >> 5] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_red[w]);
+  float l = 0.f;
+  const int c4 = tid % C4, part = tid / C4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int c = c0 + part; c <= c1; c += NS) {
+    const size_t pr = slot(c);
+    const float2 ml = __ldcg(a.part_ml + pr);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c4));
+    if (ml.x == -INFINITY) continue;  // no visible key in this part
+    const float w = ex2(ml.x - M);
+    l = fmaf(w, ml.y, l);
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
+  }
+  s_acc[tid] = acc;
+  __syncthreads();
+  if (c4 == 0) s_red[part] = l;
+  __syncthreads();
+  if (part == 0) {
+    l = 0.f;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) l += s_red[s];
+#pragma unroll
+    for (int s = 1; s < NS; ++s) {
+      const float4 x = s_acc[s * C4 + c4];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+    const int qi = row / a.group, hl = row - qi * a.group;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
+    *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  }
+}
+
+// The parts of k_kv8_attn_tc: o = sum_s w_s O_s / sum_s w_s l_s with w_s =
+// 2^(m_s - max m); one block per (sequence, KV head, row).  Splits without a visible key (m = -inf) wrote no
 // row and are passed over.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int splits, int rowsp) {
@@ -373,8 +542,10 @@ size_t few_smem(int d) { return (size_t)kWarps * 8 * (d + 4) * 4; }
 
 template <int D>
 cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st) {
-  return launch_ex(k_kv8_attn_few<D>, dim3(p.splits, p.qtiles, a.n_seq * a.c.heads), dim3(kWarps * 32), few_smem(D), st,
-                   1, pdl, a);
+  cudaError_t e = launch_ex(k_kv8_attn_few<D>, dim3(p.splits), dim3(kWarps * 32), few_smem(D), st, 1, pdl, a, p.qtiles);
+  if (e != cudaSuccess || p.ws_bytes == 0) return e;
+  return launch_ex(k_kv8_merge_few<D>, dim3(a.n_seq * a.c.heads * p.qtiles, 8), dim3(256), 0, st, 1, true, a, p.qtiles,
+                   p.splits);
 }
 template <int D>
 cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {  // (PDL behind its own attention)
@@ -386,8 +557,8 @@ cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_
 
 // Rows of a KV head (query heads in its group x queries): up to 16 take groups
 // of 8 rows on mma.sync, more (or any fresh keys) tiles of 128 rows on the
-// tcgen05 tensor cores.  Keys are split until the blocks fill the SMs, each
-// split keeping at least 128 keys of the largest cache.
+// tcgen05 tensor cores, whose keys are split until the CTAs fill the SMs,
+// each split keeping at least 64 keys of a full cache.
 Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new, int max_keys, int d) {
   Kv8AttnPlan p{};
   const long long rows = (long long)group * n_q;
@@ -397,15 +568,16 @@ Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new
   const long long blocks = (long long)n_seq * heads_kv * p.qtiles;
   const int keys = std::max(1, max_keys + n_new);
   int splits = 1;
-  if (p.tc) {
-    while (splits < 8 && blocks * splits * 2 <= 148 && keys / (splits * 2) >= 64) splits *= 2;
-  } else {
-    // several waves of blocks even out sequences of different length
-    const long long want = (4 * 148 + blocks - 1) / blocks;
-    splits = (int)std::max<long long>(1, std::min<long long>({want, (long long)kMaxKv8Splits, keys / 128}));
-    if (blocks * splits < 148) splits = (int)std::max<long long>(1, std::min<long long>(keys / 128, 148 / blocks));
-    splits = std::min(splits, kMaxKv8Splits);
+  if (!p.tc) {
+    // blocks that deal out the units of 64 keys: two (four for head_dim < 256)
+    // resident per SM, and no more than there are units in a full cache
+    const long long units = blocks * ((std::max(max_keys, 1) - 1) / kUnit + 1);
+    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
+    // (with one unit per item no item is shared)
+    p.ws_bytes = p.splits > 1 && units > blocks ? (size_t)p.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
+    return p;
   }
+  while (splits < 8 && blocks * splits * 2 <= 148 && keys / (splits * 2) >= 64) splits *= 2;
   p.splits = splits;
   p.ws_bytes = splits > 1 ? (size_t)blocks * splits * tile * ((size_t)d * 4 + 8) : 0;
   return p;
@@ -418,14 +590,8 @@ cudaError_t kv8_attn_init() {
 
 cudaError_t launch_kv8_attn(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st) {
   cudaError_t e;
-  if (p.tc)
-    e = launch_kv8_attn_tc(p, a, pdl, st);
-  else if (a.c.d == 64)
-    e = few_launch<64>(p, a, pdl, st);
-  else if (a.c.d == 128)
-    e = few_launch<128>(p, a, pdl, st);
-  else
-    e = few_launch<256>(p, a, pdl, st);
+  if (!p.tc) return a.c.d == 64 ? few_launch<64>(p, a, pdl, st) : a.c.d == 128 ? few_launch<128>(p, a, pdl, st) : few_launch<256>(p, a, pdl, st);
+  e = launch_kv8_attn_tc(p, a, pdl, st);
   if (e != cudaSuccess || p.splits == 1) return e;
   if (a.c.d == 64) return merge_launch<64>(p, a, st);
   if (a.c.d == 128) return merge_launch<128>(p, a, st);

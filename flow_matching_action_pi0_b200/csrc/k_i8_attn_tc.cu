@@ -8,14 +8,17 @@
 //   converters (8 warps)  read the codes (16-byte loads, the next chunk's in
 //                         flight while this one is written), turn them into
 //                         bf16 integers (exact) in the 128-byte swizzled tiles
-//                         the MMA reads, and put the keys' scales beside them;
-//                         fresh keys and values are copied as they are, scale 1
+//                         the MMA reads; fresh keys and values are copied as
+//                         they are
 //   MMA thread            S = Q K^T (128 x 64, double-buffered in TMEM), then
 //                         O += P V (P read from TMEM, V read MN-major)
-//   softmax (8 warps)     two threads per row: scores x key scale, online
+//   scale warp            the chunk's key and value scales
+//   softmax (16 warps)    four threads per row: scores x key scale, online
 //                         softmax in the log2 domain (O is rescaled only when
 //                         the maximum grows by more than 2^8), P x value scale
-//                         as bf16 over S's own columns
+//                         as bf16 over S's own columns.  The chunk-to-chunk
+//                         chain runs through it, so its latency counts: with
+//                         two threads per row a chunk took 2900 cycles.
 // Bound: the softmax and conversion work per tile, between the tensor cores'
 // and the cache's floors (K and V of a sequence are converted once per tile).
 // Key splits (small batches) write unnormalised fp32 rows with their maximum
@@ -28,9 +31,12 @@ namespace pae {
 namespace {
 
 constexpr int QROWS = 128, CK = 64;
-constexpr int kSmx = 256;                  // softmax threads (warps 0-7)
+constexpr int kSmxWarps = 16;              // softmax warps (0-15): four threads per row
+constexpr int kSmx = kSmxWarps * 32;
+constexpr int kMmaWarp = kSmxWarps, kScaleWarp = kMmaWarp + 1, kConvWarp = kScaleWarp + 1;
 constexpr int kConv = 128;                 // converter threads per operand
-constexpr int kThreads = kSmx + 32 + 2 * kConv;
+constexpr int kThreads = kConvWarp * 32 + 2 * kConv;
+constexpr int KP = CK / 4;                 // keys per softmax part
 constexpr long long kDrainNs = 4000000000LL;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -39,7 +45,33 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  return (uint32_t)__bfloat16_as_ushort(f2bf(lo)) | ((uint32_t)__bfloat16_as_ushort(f2bf(hi)) << 16);
+  uint32_t r;  // one instruction for the pair, round to nearest even
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two fp32 operations in one instruction: (a, b) op (c, d).
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // Two signed bytes in bits 0-7 and 16-23 -> bf16x2, exactly (see k_i8_attn.cu).
 __device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
@@ -49,14 +81,14 @@ __device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// AND over the 64 threads of the two warps that share 32 rows.
-__device__ __forceinline__ bool pair_and(int id, bool v) {
+// AND over the 128 threads of the four warps that share 32 rows.
+__device__ __forceinline__ bool rows_and(int id, bool v) {
   __syncwarp();
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 64, p;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)v), "r"(id)
@@ -64,16 +96,47 @@ __device__ __forceinline__ bool pair_and(int id, bool v) {
   return r != 0;
 }
 
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* v) {
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// D[tmem] (+)= A B^T, bf16, descriptors as (low word, common high word).  The
+// accumulate flag is a compile-time constant, so an MMA costs little more than
+// its own issue.
+template <bool ACC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
-          taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "n"(ACC ? 1 : 0)
       : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 template <int D>
@@ -81,8 +144,8 @@ struct Smem {
   static constexpr uint32_t kTile = CK * D * 2;  // one chunk of K (or V) in bf16
   static constexpr uint32_t q = 0, k = QROWS * D * 2, v = k + 2 * kTile, sc = v + 2 * kTile;
   static constexpr uint32_t pm = sc + 2 * 2 * CK * 4;    // scales: 2 chunks of [ks 64 | vs 64]
-  static constexpr uint32_t l = pm + 2 * 2 * QROWS * 4;  // partial maxima [2][2][128]
-  static constexpr uint32_t bar = l + 2 * QROWS * 4;     // partial sums [2][128]
+  static constexpr uint32_t l = pm + 2 * 4 * QROWS * 4;  // partial maxima [2][4][128]
+  static constexpr uint32_t bar = l + 4 * QROWS * 4;     // partial sums [4][128]
   static constexpr uint32_t total = bar + 256 + 1024;
 };
 
@@ -101,14 +164,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   uint64_t* s_full = bars + 9;      // [2] S computed
   uint64_t* p_full = bars + 11;     // [2] P written over S
   uint64_t* o_done = bars + 13;     // [2] PV of the buffer's chunk done
-  uint64_t* drain = bars + 15;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  uint64_t* sc_full = bars + 15;    // [2] the chunk's scales in place
+  uint64_t* drain = bars + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sc = reinterpret_cast<float*>(smem + L::sc);
   float* s_pm = reinterpret_cast<float*>(smem + L::pm);
   float* s_l = reinterpret_cast<float*>(smem + L::l);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // (a shuffle tells the compiler that the warp index is the same in all lanes)
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int qt = blockIdx.x, split = blockIdx.y, splits = gridDim.y, bg = blockIdx.z;
   const int b = bg / a.c.heads, h = bg - b * a.c.heads;
   const int rows = a.group * a.n_q;
@@ -124,12 +189,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], kSmx);
       mbar_init(&o_done[i], 1);
+      mbar_init(&sc_full[i], 32);
     }
     mbar_init(drain, 1);
     s_flag[0] = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
+  if (warp == kMmaWarp) {
     tmem_alloc(tmem_slot, ncols);
     tmem_relinquish();
   }
@@ -150,39 +216,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   const int c0 = (int)((long long)(nc + nf) * split / splits), c1 = (int)((long long)(nc + nf) * (split + 1) / splits);
   const int nch = c1 - c0;
 
-  if (warp >= 9) {
+  if (warp >= kConvWarp) {
     // ------------------------------------------------------------ converters
     // A warp's 16-byte pieces cover 8 rows x 64 channels: lane = 4 row + piece.
     // Rows of different parity land in different halves of the swizzled 128-byte
     // rows, so the two 16-byte stores of 8 lanes touch all banks once.
-    const bool is_v = warp >= 13;
-    const int cw = (warp - 9) & 3;                       // warp within the operand's four
+    const bool is_v = warp >= kConvWarp + 4;
+    const int cw = (warp - kConvWarp) & 3;               // warp within the operand's four
     const int cp = lane & 3, rl = lane >> 2;
     constexpr int UNITS = NBOX * 8 / 4;                  // (box, 8 rows) units per warp
     const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
     const int8_t* src = (is_v ? a.c.v : a.c.k) + base * D;
-    const float* ksc = a.c.k_scale + base;
-    const float* vsc = a.c.v_scale + base;
     const bf16* fresh = is_v ? a.v_new : a.k_new;
     const long long f_tok = is_v ? a.vn_tok : a.kn_tok;
     if (fresh) fresh += b * (is_v ? a.vn_seq : a.kn_seq) + (long long)h * (is_v ? a.vn_head : a.kn_head);
     uint64_t* full = is_v ? v_full : k_full;
     uint64_t* empty = is_v ? v_empty : k_empty;
     const uint32_t tile0 = smem_u32(smem + (is_v ? L::v : L::k));
-    const int ct = cw * 32 + lane;
+    // unit u of this warp: box box0, rows row0 + 8 u
+    const int box0 = cw * UNITS >> 3, row0 = (cw * UNITS & 7) * 8 + rl;
+    const int8_t* src0 = src + (size_t)row0 * D + box0 * 64 + cp * 16;
+    const uint32_t dst0 = tile0 + (uint32_t)(box0 * CK * 128 + row0 * 128);
+    const uint32_t sw0 = (uint32_t)((2 * cp) ^ rl) << 4, sw1 = (uint32_t)((2 * cp + 1) ^ rl) << 4;
     uint4 raw[UNITS];
-    float sc = 0.f;  // V converters: thread j < 64 carries key j's K scale, 64 + j its V scale
-    auto load = [&](int c) {  // a cached chunk's codes and scales
+    auto load = [&](int c) {  // a cached chunk's codes
       const int key0 = c * CK;
+      const int8_t* p = src0 + (size_t)key0 * D;
+      if (key0 + CK <= seen) {
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int unit = cw * UNITS + u, box = unit >> 3, row = (unit & 7) * 8 + rl;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (key0 + row < seen) raw[u] = __ldg(reinterpret_cast<const uint4*>(src + (size_t)(key0 + row) * D + box * 64 + cp * 16));
-      }
-      if (is_v) {
-        const int key = key0 + (ct & (CK - 1));
-        sc = key < seen ? (ct < CK ? __ldg(ksc + key) * a.scale_log2 : __ldg(vsc + key)) : 0.f;
+        for (int u = 0; u < UNITS; ++u) raw[u] = __ldg(reinterpret_cast<const uint4*>(p + u * 8 * D));
+      } else {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          raw[u] = make_uint4(0, 0, 0, 0);
+          if (key0 + row0 + 8 * u < seen) raw[u] = __ldg(reinterpret_cast<const uint4*>(p + u * 8 * D));
+        }
       }
     };
     if (nch > 0 && c0 < nc) load(c0);
@@ -193,12 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         set_error(a.err, DEV_TIMEOUT);
         break;
       }
-      const uint32_t tile = tile0 + (uint32_t)slot * L::kTile;
+      const uint32_t dst = dst0 + (uint32_t)slot * L::kTile;
       if (c < nc) {
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-          const int unit = cw * UNITS + u, box = unit >> 3, row = (unit & 7) * 8 + rl;
-          const uint32_t at = tile + (uint32_t)(box * CK * 128 + row * 128);
+          const uint32_t at = dst + u * 8 * 128;
           const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
           uint32_t o[8];
 #pragma unroll
@@ -206,96 +273,145 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
             o[2 * q] = bytes_bf16x2(__byte_perm(w[q], 0, 0x4140));
             o[2 * q + 1] = bytes_bf16x2(__byte_perm(w[q], 0, 0x4342));
           }
-          sts128(at + (uint32_t)(((2 * cp) ^ (row & 7)) << 4), o[0], o[1], o[2], o[3]);
-          sts128(at + (uint32_t)(((2 * cp + 1) ^ (row & 7)) << 4), o[4], o[5], o[6], o[7]);
+          sts128(at + sw0, o[0], o[1], o[2], o[3]);
+          sts128(at + sw1, o[4], o[5], o[6], o[7]);
         }
       } else {
         const int t0 = (c - nc) * CK;
 #pragma unroll 4
         for (int u = 0; u < UNITS; ++u) {
-          const int unit = cw * UNITS + u, box = unit >> 3, row = (unit & 7) * 8 + rl;
-          const uint32_t at = tile + (uint32_t)(box * CK * 128 + row * 128);
+          const int row = row0 + 8 * u;
+          const uint32_t at = dst + u * 8 * 128;
           uint4 x = make_uint4(0, 0, 0, 0), y = x;
           if (t0 + row < a.n_new) {
-            const bf16* p = fresh + (long long)(t0 + row) * f_tok + box * 64 + cp * 16;
+            const bf16* p = fresh + (long long)(t0 + row) * f_tok + box0 * 64 + cp * 16;
             x = *reinterpret_cast<const uint4*>(p);
             y = *reinterpret_cast<const uint4*>(p + 8);
           }
-          sts128(at + (uint32_t)(((2 * cp) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
-          sts128(at + (uint32_t)(((2 * cp + 1) ^ (row & 7)) << 4), y.x, y.y, y.z, y.w);
+          sts128(at + sw0, x.x, x.y, x.z, x.w);
+          sts128(at + sw1, y.x, y.y, y.z, y.w);
         }
-        sc = t0 + (ct & (CK - 1)) >= a.n_new ? 0.f : ct < CK ? a.scale_log2 : 1.f;
       }
-      // The V converters bring both scales: a chunk's softmax waits for v_full,
-      // and its scales are overwritten only after its PV.
-      if (is_v) s_sc[slot * 2 * CK + ct] = sc;
       fence_proxy_async_smem();
       mbar_arrive(&full[slot]);
       if (i + 1 < nch && c + 1 < nc) load(c + 1);
     }
-  } else if (warp == 8) {
+  } else if (warp == kScaleWarp) {
+    // ---------------------------------------------------------------- scales
+    // lane l: key and value scales of keys l and l + 32, the next chunk's in
+    // flight; a slot is written again only after its chunk's PV
+    const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
+    float k[2], v[2];
+    auto load = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = lane + 32 * j;
+        const bool in = c < nc ? c * CK + at < seen : (c - nc) * CK + at < a.n_new;
+        k[j] = !in ? 0.f : c < nc ? __ldg(a.c.k_scale + base + c * CK + at) * a.scale_log2 : a.scale_log2;
+        v[j] = !in ? 0.f : c < nc ? __ldg(a.c.v_scale + base + c * CK + at) : 1.f;
+      }
+    };
+    if (nch > 0) load(c0);
+    for (int i = 0; i < nch; ++i) {
+      const int slot = i & 1;
+      if (!__all_sync(0xffffffffu, i < 2 || mbar_wait(&o_done[slot], ((i >> 1) & 1) ^ 1, a.err.wait_ns))) {
+        s_flag[0] = 1;
+        set_error(a.err, DEV_TIMEOUT);
+        break;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s_sc[slot * 2 * CK + lane + 32 * j] = k[j];
+        s_sc[slot * 2 * CK + CK + lane + 32 * j] = v[j];
+      }
+      mbar_arrive(&sc_full[slot]);
+      if (i + 1 < nch) load(c0 + i + 1);
+    }
+  } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------------- MMA
-    if (lane == 0 && nch > 0) {
+    // The whole warp walks the loop and one lane issues: addresses then live in
+    // uniform registers.  (Issued from a one-lane branch, the 20 MMAs of a chunk
+    // took 1900 cycles of a scheduler that six other warps keep busy.)
+    if (nch > 0) {
       constexpr uint32_t idesc_s = idesc_bf16(QROWS, CK), idesc_o = idesc_bf16(QROWS, D, 0, 1);
       bool good = mbar_wait(q_full, 0, a.err.wait_ns);
       const uint64_t q_desc = sw128_desc(smem_u32(smem + L::q), 16, 1024);
       const uint64_t k_desc = sw128_desc(smem_u32(smem + L::k), 16, 1024);
       const uint64_t v_desc = sw128_desc(smem_u32(smem + L::v), CK * 128, 1024);
+      const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;
+      const uint32_t qk_hi = (uint32_t)(q_desc >> 32), v_hi = (uint32_t)(v_desc >> 32);
       // S of chunk i goes over P of chunk i - 2: that chunk's PV must be done
       auto issue_s = [&](int i) -> bool {
         const int st = i & 1;
-        if (!mbar_wait(&k_full[st], (i >> 1) & 1, a.err.wait_ns)) return false;
-        if (i >= 2 && !mbar_wait(&o_done[st], ((i >> 1) & 1) ^ 1, a.err.wait_ns)) return false;
+        bool ok = mbar_wait(&k_full[st], (i >> 1) & 1, a.err.wait_ns);
+        if (ok && i >= 2) ok = mbar_wait(&o_done[st], ((i >> 1) & 1) ^ 1, a.err.wait_ns);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)(st * CK), kl = k_lo + (uint32_t)st * (L::kTile >> 4);
+        if (elect_one()) {
+          mma_ss<false>(d, q_lo, kl, qk_hi, idesc_s);
 #pragma unroll
-        for (int k16 = 0; k16 < D / 16; ++k16) {
-          const uint32_t x = (uint32_t)k16 >> 2, w = ((uint32_t)k16 & 3u) * 32u;
-          umma_bf16(tmem + (uint32_t)(st * CK), desc_add(q_desc, x * QROWS * 128u + w),
-                    desc_add(k_desc, st * L::kTile + x * CK * 128u + w), idesc_s, k16 > 0 ? 1u : 0u);
+          for (uint32_t k16 = 1; k16 < D / 16; ++k16) {
+            const uint32_t x = k16 >> 2, w = (k16 & 3u) * 32u;
+            mma_ss<true>(d, q_lo + ((x * QROWS * 128u + w) >> 4), kl + ((x * CK * 128u + w) >> 4), qk_hi, idesc_s);
+          }
+          umma_commit(&s_full[st]);
+          umma_commit(&k_empty[st]);
         }
-        umma_commit(&s_full[st]);
-        umma_commit(&k_empty[st]);
+        __syncwarp();
         return true;
       };
+      good = __all_sync(0xffffffffu, good);
       if (good) good = issue_s(0);
       for (int i = 0; good && i < nch; ++i) {
         const int st = i & 1;
         if (i + 1 < nch && !(good = issue_s(i + 1))) break;
-        if (!mbar_wait(&p_full[st], (i >> 1) & 1, a.err.wait_ns) || !mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns)) {
-          good = false;
-          break;
-        }
+        good = mbar_wait(&p_full[st], (i >> 1) & 1, a.err.wait_ns) && mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns);
+        if (!(good = __all_sync(0xffffffffu, good))) break;
         tc_fence_after();
+        const uint32_t p = tmem + (uint32_t)(st * CK), vl = v_lo + (uint32_t)st * (L::kTile >> 4);
+        if (elect_one()) {
+          mma_ts(t_o, p, vl, v_hi, idesc_o, i > 0 ? 1u : 0u);
 #pragma unroll
-        for (int k16 = 0; k16 < CK / 16; ++k16)
-          umma_bf16_tmem_a(t_o, tmem + (uint32_t)(st * CK) + k16 * 8u, desc_add(v_desc, st * L::kTile + k16 * 16u * 128u),
-                           idesc_o, (i > 0 || k16 > 0) ? 1u : 0u);
-        umma_commit(&o_done[st]);
-        umma_commit(&v_empty[st]);
+          for (uint32_t k16 = 1; k16 < CK / 16; ++k16) mma_ts(t_o, p + k16 * 8u, vl + ((k16 * 16u * 128u) >> 4), v_hi, idesc_o, 1u);
+          umma_commit(&o_done[st]);
+          umma_commit(&v_empty[st]);
+        }
+        __syncwarp();
       }
       if (!good) {
         s_flag[0] = 1;
         set_error(a.err, DEV_TIMEOUT);
       }
-      // every MMA this thread issued must finish before TMEM is freed
-      umma_commit(drain);
-      if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+      // every MMA issued must finish before TMEM is freed (the commits come from
+      // whichever lane was elected: one of the warp's, the same each time)
+      if (elect_one()) {
+        umma_commit(drain);
+        if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+      }
     }
     __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
-    {
-      // Q tile: 16-byte chunks, rows past the last are zeros
+    if (nch > 0) {
+      // Q tile: 16-byte chunks, all of a thread's in flight at once; rows past
+      // the last are zeros
+      constexpr int NQ = QROWS * D / 8 / kSmx;
       const uint32_t q0 = smem_u32(smem + L::q);
-#pragma unroll 8
-      for (int e = threadIdx.x; e < QROWS * D / 8; e += kSmx) {
-        const int row = e / (D / 8), ch = e - row * (D / 8), rq = qt * QROWS + row;
-        uint4 x = make_uint4(0, 0, 0, 0);
+      uint4 x[NQ];
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int e = threadIdx.x + i * kSmx, row = e / (D / 8), ch = e % (D / 8), rq = qt * QROWS + row;
+        x[i] = make_uint4(0, 0, 0, 0);
         if (rq < rows) {
           const int qi = rq / a.group, hl = rq - qi * a.group;
-          x = *reinterpret_cast<const uint4*>(a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + ch * 8);
+          x[i] = *reinterpret_cast<const uint4*>(a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + ch * 8);
         }
-        sts128(q0 + (uint32_t)((ch >> 3) * QROWS * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), x.x, x.y, x.z, x.w);
+      }
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int e = threadIdx.x + i * kSmx, row = e / (D / 8), ch = e % (D / 8);
+        sts128(q0 + (uint32_t)((ch >> 3) * QROWS * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4)), x[i].x, x[i].y, x[i].z, x[i].w);
       }
       fence_proxy_async_smem();
       mbar_arrive(q_full);
@@ -304,73 +420,83 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     const int r = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const int rq = qt * QROWS + r;
-    const int oc0 = part * (D / 2);
+    const int oc0 = part * (D / 4);
     const int lim = a.causal ? min(len, len - a.n_q + 1 + min(rq, rows - 1) / a.group) : len;
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     for (int i = 0; i < nch; ++i) {
       const int st = i & 1, c = c0 + i;
-      const bool got = mbar_wait(&s_full[st], (i >> 1) & 1, a.err.wait_ns) &&
-                       mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns);
+      const bool got = mbar_wait(&sc_full[st], (i >> 1) & 1, a.err.wait_ns) &&
+                       mbar_wait(&s_full[st], (i >> 1) & 1, a.err.wait_ns);
       __syncwarp();
       tc_fence_after();
-      float sv[32];
-      tmem_ld16(tmem + (uint32_t)(st * CK) + lane_off + part * 32, sv);
-      tmem_ld16(tmem + (uint32_t)(st * CK) + lane_off + part * 32 + 16, sv + 16);
+      float sv[KP];
+      tmem_ld16(tmem + (uint32_t)(st * CK) + lane_off + part * KP, sv);
       tmem_ld_wait();
       reg_fence16(sv);
-      reg_fence16(sv + 16);
-      const float* sc = s_sc + st * 2 * CK + part * 32;
-      // visible keys of this part's 32
-      const int vis = (c < nc ? lim - c * CK : a.n_new - (c - nc) * CK) - part * 32;
+      const float* sc = s_sc + st * 2 * CK + part * KP;
+      // visible keys of this part's
+      const int vis = (c < nc ? lim - c * CK : a.n_new - (c - nc) * CK) - part * KP;
+      float2* s2 = reinterpret_cast<float2*>(sv);
 #pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 k4 = *reinterpret_cast<const float4*>(sc + j);
-        sv[j] *= k4.x;
-        sv[j + 1] *= k4.y;
-        sv[j + 2] *= k4.z;
-        sv[j + 3] *= k4.w;
+      for (int j = 0; j < KP / 2; j += 2) {
+        const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * j);
+        s2[j] = mul2(s2[j], make_float2(k4.x, k4.y));
+        s2[j + 1] = mul2(s2[j + 1], make_float2(k4.z, k4.w));
       }
-      if (vis < 32) {
+      if (vis < KP) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) sv[j] = j < vis ? sv[j] : -INFINITY;
+        for (int j = 0; j < KP; ++j) sv[j] = j < vis ? sv[j] : -INFINITY;
       }
-      float mt[16];
+      float mt[KP / 4];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) mt[j] = fmaxf(sv[j], sv[j + 16]);
-#pragma unroll
-      for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-        for (int j = 0; j < w; ++j) mt[j] = fmaxf(mt[j], mt[j + w]);
-      s_pm[(st * 2 + part) * QROWS + r] = mt[0];
-      // both parts of the row have their scores in registers (P overwrites S)
-      // and their maxima in place, and go on or stop together
-      if (!pair_and(1 + (warp & 3), got && s_flag[0] == 0)) {
+      for (int j = 0; j < KP / 4; ++j) mt[j] = fmaxf(max3(sv[4 * j], sv[4 * j + 1], sv[4 * j + 2]), sv[4 * j + 3]);
+      float* pm = s_pm + st * 4 * QROWS + r;
+      pm[part * QROWS] = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]);
+      // every part of the row has its scores in registers (P overwrites S) and
+      // its maximum in place, and all go on or stop together
+      if (!rows_and(1 + (warp & 3), got && s_flag[0] == 0)) {
         ok = false;
         break;
       }
-      const float cmax = fmaxf(s_pm[st * 2 * QROWS + r], s_pm[(st * 2 + 1) * QROWS + r]);
+      const float cmax = fmaxf(max3(pm[0], pm[QROWS], pm[2 * QROWS]), pm[3 * QROWS]);
       const float mx = cmax > m_run + 8.f ? cmax : m_run;
       const float ref = mx == -INFINITY ? 0.f : mx;  // no visible key so far
       const float alpha = ex2(m_run - ref);          // 1 when unchanged, 0 at first
+      const float2 nref = make_float2(-ref, -ref);
+      float2 sum[2];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) sv[j] = ex2(sv[j] - ref);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) mt[j] = sv[j] + sv[j + 16];
-#pragma unroll
-      for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-        for (int j = 0; j < w; ++j) mt[j] += mt[j + w];
-      l_run = l_run * (m_run == -INFINITY ? 1.f : alpha) + mt[0];
+      for (int j = 0; j < KP / 2; ++j) {
+        s2[j] = add2(s2[j], nref);
+        s2[j].x = ex2(s2[j].x);
+        s2[j].y = ex2(s2[j].y);
+        sum[j & 1] = j < 2 ? s2[j] : add2(sum[j & 1], s2[j]);
+      }
+      sum[0] = add2(sum[0], sum[1]);
+      l_run = l_run * (m_run == -INFINITY ? 1.f : alpha) + (sum[0].x + sum[0].y);
       const bool scale_o = i > 0 && alpha != 1.f && m_run != -INFINITY;
       m_run = mx;
+#pragma unroll
+      for (int j = 0; j < KP / 2; j += 2) {
+        const float4 v4 = *reinterpret_cast<const float4*>(sc + CK + 2 * j);
+        s2[j] = mul2(s2[j], make_float2(v4.x, v4.y));
+        s2[j + 1] = mul2(s2[j + 1], make_float2(v4.z, v4.w));
+      }
+      if (vis < KP) {  // masked places stay 0 whatever their scale is
+#pragma unroll
+        for (int j = 0; j < KP; ++j) sv[j] = j < vis ? sv[j] : 0.f;
+      }
+      uint32_t pk[KP / 2];
+#pragma unroll
+      for (int j = 0; j < KP / 2; ++j) pk[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
+      tmem_st8u(tmem + (uint32_t)(st * CK) + lane_off + part * (KP / 2), pk);
       if (__any_sync(0xffffffffu, scale_o)) {
         // O may be rescaled only once PV of the previous chunk has landed in it
         const bool good = __all_sync(0xffffffffu, mbar_wait(&o_done[st ^ 1], ((i - 1) >> 1) & 1, a.err.wait_ns));
         if (good) {
           const float f = scale_o ? alpha : 1.f;
           tc_fence_after();
-          for (int jj = oc0; jj < oc0 + D / 2; jj += 16) {
+          for (int jj = oc0; jj < oc0 + D / 4; jj += 16) {
             float ov[16];
             tmem_ld16(t_o + lane_off + jj, ov);
             tmem_ld_wait();
@@ -379,27 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
             for (int t = 0; t < 16; ++t) ov[t] *= f;
             tmem_st16(t_o + lane_off + jj, ov);
           }
-          tmem_st_wait();
         } else {
           s_flag[0] = 1;
         }
       }
-      uint32_t pk[16];
-#pragma unroll
-      for (int j = 0; j < 32; j += 4) {
-        const float4 v4 = *reinterpret_cast<const float4*>(sc + CK + j);
-        sv[j] *= v4.x;
-        sv[j + 1] *= v4.y;
-        sv[j + 2] *= v4.z;
-        sv[j + 3] *= v4.w;
-      }
-      if (vis < 32) {  // masked places stay 0 whatever their scale is
-#pragma unroll
-        for (int j = 0; j < 32; ++j) sv[j] = j < vis ? sv[j] : 0.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
-      tmem_st16u(tmem + (uint32_t)(st * CK) + lane_off + part * 16, pk);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[st]);
@@ -408,50 +517,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     // PVs complete in issue order: the last chunk's commit covers them all
     if (nch > 0 && ok) ok = mbar_wait(&o_done[(nch - 1) & 1], ((nch - 1) >> 1) & 1, kDrainNs);
     s_l[part * QROWS + r] = l_run;
-    ok = pair_and(1 + (warp & 3), ok && s_flag[0] == 0);
+    ok = rows_and(1 + (warp & 3), ok && s_flag[0] == 0);
     tc_fence_after();
-    const float l = s_l[r] + s_l[QROWS + r];
+    const float l = ((s_l[r] + s_l[QROWS + r]) + s_l[2 * QROWS + r]) + s_l[3 * QROWS + r];
     // NaN scores alone leave the maximum at -inf: the row is not empty
     if (m_run == -INFINITY && l != 0.f) m_run = 0.f;
-    const int qi = rq / a.group, hl = rq - qi * a.group;
-    const bool live = rq < rows;
-    if (splits == 1) {
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
-      bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head;
-      for (int jj = oc0; jj < oc0 + D / 2; jj += 16) {
-        float ov[16];
-        if (ok && nch > 0) {
-          tmem_ld16(t_o + lane_off + jj, ov);
-          tmem_ld_wait();
-          reg_fence16(ov);
-        } else {
+    // Output rows go through shared memory (every MMA is done: the tiles are
+    // free), so that a row leaves as one run of 16-byte stores; straight from
+    // the registers, a warp's store touches 32 rows and the 128 rows of a tile
+    // took 7000 cycles.  Chunks of 16 bytes are swizzled by the row.
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
+    const bool some = ok && nch > 0 && m_run != -INFINITY;
+    const size_t pr0 = ((size_t)bg * splits + split) * ((size_t)gridDim.x * QROWS) + qt * QROWS;
+    if (splits > 1 && part == 0) a.part_ml[pr0 + r] = some ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+    const uint32_t stage = smem_u32(smem);
+    const int esz = splits == 1 ? 2 : 4;
+    const uint32_t rowb = (uint32_t)(D * esz), srow = stage + (uint32_t)r * rowb;
 #pragma unroll
-          for (int t = 0; t < 16; ++t) ov[t] = 0.f;
-        }
-        if (live && ok) {
-          uint32_t w[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) w[t] = pack_bf16(ov[2 * t] * inv, ov[2 * t + 1] * inv);
-          uint4* dst = reinterpret_cast<uint4*>(op + jj);
-          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        }
-      }
-    } else {
-      const size_t pr = ((size_t)bg * splits + split) * ((size_t)gridDim.x * QROWS) + rq;
-      const bool some = ok && nch > 0 && m_run != -INFINITY;
-      if (part == 0) a.part_ml[pr] = some ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+    for (int j = 0; j < D / 4; j += 16) {
+      float ov[16];
       if (ok && nch > 0) {
-        for (int jj = oc0; jj < oc0 + D / 2; jj += 16) {
-          float ov[16];
-          tmem_ld16(t_o + lane_off + jj, ov);
-          tmem_ld_wait();
-          reg_fence16(ov);
-          if (some) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + pr * D + jj);
+        tmem_ld16(t_o + lane_off + oc0 + j, ov);
+        tmem_ld_wait();
+        reg_fence16(ov);
+      } else {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) dst[t] = make_float4(ov[4 * t], ov[4 * t + 1], ov[4 * t + 2], ov[4 * t + 3]);
-          }
+        for (int t = 0; t < 16; ++t) ov[t] = 0.f;
+      }
+      if (splits == 1) {
+        const uint32_t ch = (uint32_t)(oc0 + j) / 8;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          sts128(srow + (((ch + t) ^ (r & 7)) << 4), pack_bf16(ov[8 * t] * inv, ov[8 * t + 1] * inv),
+                 pack_bf16(ov[8 * t + 2] * inv, ov[8 * t + 3] * inv), pack_bf16(ov[8 * t + 4] * inv, ov[8 * t + 5] * inv),
+                 pack_bf16(ov[8 * t + 6] * inv, ov[8 * t + 7] * inv));
+      } else {
+        const uint32_t ch = (uint32_t)(oc0 + j) / 4;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          sts128(srow + (((ch + t) ^ (r & 7)) << 4), __float_as_uint(ov[4 * t]), __float_as_uint(ov[4 * t + 1]),
+                 __float_as_uint(ov[4 * t + 2]), __float_as_uint(ov[4 * t + 3]));
+      }
+    }
+    ok = rows_and(1 + (warp & 3), ok);
+    if (ok) {
+      // the four warps of these 32 rows take 8 rows each
+      const int cpr = (int)rowb / 16;  // chunks per row: 8 to 64
+      const int base = (warp & 3) * 32 + part * 8;
+      for (int e = lane; e < 8 * cpr; e += 32) {
+        const int row = base + e / cpr, ch = e % cpr, q = qt * QROWS + row;
+        if (q >= rows) continue;
+        const uint4 x = lds128(stage + (uint32_t)row * rowb + (uint32_t)((ch ^ (row & 7)) << 4));
+        if (splits == 1) {
+          const int qi = q / a.group, hl = q - qi * a.group;
+          *reinterpret_cast<uint4*>(a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + ch * 8) = x;
+        } else {
+          *reinterpret_cast<uint4*>(a.part_o + (pr0 + row) * D + ch * 4) = x;
         }
       }
     }
@@ -459,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, ncols);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, ncols);
 }
 
 template <int D>
