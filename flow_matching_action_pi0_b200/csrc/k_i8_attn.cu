@@ -4,21 +4,26 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j - max),
 //   k_j = kq_j ks_j, v_j = vq_j vs_j  (8-bit codes, one scale per key)
 //
-// One pass over the keys with the running maximum and sum of a softmax.  The
-// codes enter the products as bf16 integers, which is exact; the key's scale
-// multiplies its score afterwards, the value's scale its probability (rounded
-// once to bf16, as an attention with bf16 values rounds its probabilities).
+// One pass over the keys with the running maximum and sum of a softmax.
+// Scores: a query row becomes 16-bit integers of its own scale, q = (256 hi +
+// lo) qs with two signed 8-bit digits, |q| error at most max|q| 2^-16, so the
+// key codes go into integer products as they lie in memory, two per 32
+// channels, and the sums are exact.  (As bf16 operands every pair of codes
+// costs four instructions, half of the loop.)  Values: the codes become bf16
+// integers, which is exact, and the value's scale multiplies its probability
+// (rounded once to bf16, as an attention with bf16 values rounds its
+// probabilities).
 //
 // Bound: bytes of the cache (2 (d + 4) per key and KV head).  The G query
 // heads of a KV head share every byte, 8 rows at a time as the N side of
-// mma.sync m16n8k16 (keys, then value channels, on the M side): a warp turns
-// the 16 bytes that a lane loads straight into A fragments in registers, with
-// no trip through shared memory (a 128-row tensor-core tile would be 94 %
+// mma.sync (m16n8k32 for keys, m16n8k16 for value channels, on the M side): a lane turns
+// the 16 bytes that it copied itself straight into A fragments, with no
+// exchange between lanes (a 128-row tensor-core tile would be 94 %
 // padding here and its operands would have to be staged).  The contraction
 // index may be permuted freely, so fragments are cut from contiguous 16-byte
 // loads:
 //   K: lane (g, t) = (lane / 4, lane % 4) loads 16 channels [64 j + 16 t, +16)
-//      of keys g and g + 8; step s of block j takes bytes 4 s .. 4 s + 3
+//      of keys g and g + 8: two products of 32 channels
 //   V: lane (g, t) loads 16 channels [128 h + 16 g, +16) of keys 2t, 2t + 1,
 //      2t + 8, 2t + 9; product m of block h takes channels 2 m (row g) and
 //      2 m + 1 (row g + 8)
@@ -56,6 +61,14 @@ __device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// int8 x int8 -> int32, 32 channels
+__device__ __forceinline__ void mma_s8(int* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 8 x 8 transpose of 16-bit elements across the warp
@@ -116,16 +129,29 @@ __device__ __forceinline__ long long scan_units(const Kv8AttnArgs& a, long long*
   return total;
 }
 
+constexpr int kStages = 2;  // tiles of 16 keys per warp, the one at work included
+constexpr long long kDrainNs = 4000000000LL;
+// K codes | V codes of a tile: [16 keys][d] each, as they lie in the cache
+__host__ __device__ constexpr int few_stage(int d) { return 2 * kTileKeys * d; }
+
+// Untiled bulk copy global -> shared, completion on `bar` (16-byte units).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(const Kv8AttnArgs a, int rgs) {
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(const Kv8AttnArgs a, int rgs) {
   constexpr int KBLK = D / 64;               // 64-channel blocks of a K row
   constexpr int VB = D >= 128 ? 16 : 8;      // bytes of a V row per lane and block
   constexpr int VBLK = D / (8 * VB);         // blocks of a V row
   constexpr int VM = VB / 2;                 // products per block
   constexpr int STEP = kUnit;
-  extern __shared__ float s_o[];             // [kWarps][8][D + 4]
+  extern __shared__ __align__(16) float s_o[];  // the warps' rings; at the end of a sequence [kWarps][8][D + 4]
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
   __shared__ float2 s_row[8];
+  __shared__ uint64_t s_bar[kWarps][kStages];
   __shared__ long long s_scan[kWarps];
   __shared__ int s_b;
   __shared__ long long s_before;
@@ -133,6 +159,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
   const int g = lane >> 2, t = lane & 3;
   const int rows = a.group * a.n_q;
   const int hr = a.c.heads * rgs;  // items (KV head, row group) of a sequence
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp][i], 1);
+    fence_mbar_init();
+  }
   pdl_launch_dependents();
   pdl_wait();
 
@@ -162,6 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     b_unit = s_before;
   }
 
+  int tiles = 0;  // tiles this warp has asked for: tile i goes through stage i % kStages
   while (unit < unit_end) {
   const int len = seq_len(a, b), units = seq_units(len);
   const int item = (int)((unit - b_unit) / units), u0 = (int)((unit - b_unit) - (long long)item * units);
@@ -169,24 +200,81 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
   const int h = item / rgs, rg = item - h * rgs;
   const int key0 = min(len, u0 * STEP), key1 = (int)min((long long)len, (long long)u1 * STEP);
 
+  const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
+  // Each warp streams its own tiles through a ring of its own: one bulk copy
+  // for the K codes of 16 keys and one for their V codes (copied by the lanes
+  // 16 bytes at a time, the same bytes kept the load/store unit busy for as
+  // long as the memory).  Rows past the range are not copied: what the stage
+  // holds there is masked.  The scales ride in a register, one per lane.
+  int8_t* ring = reinterpret_cast<int8_t*>(s_o) + warp * (kStages * few_stage(D));
+  auto fill = [&](int at) {
+    if (lane == 0) {
+      const uint32_t bytes = (uint32_t)min(kTileKeys, key1 - at) * D;
+      const int st = tiles % kStages;
+      const uint32_t dst = smem_u32(ring + st * few_stage(D));
+      mbar_arrive_expect_tx(&s_bar[warp][st], 2 * bytes);
+      bulk_load(dst, a.c.k + (base + at) * D, bytes, &s_bar[warp][st]);
+      bulk_load(dst + kTileKeys * D, a.c.v + (base + at) * D, bytes, &s_bar[warp][st]);
+    }
+    ++tiles;
+  };
+  auto scales = [&](int at) {  // lanes 0-15: K scales of keys at.., 16-31: V scales
+    const int key = min(at + (lane & 15), key1 - 1);
+    return __ldg((lane < 16 ? a.c.k_scale : a.c.v_scale) + base + key);
+  };
+  int at = key0 + warp * kTileKeys;
+  float sc_next = 0.f;
+  if (at < key1) {
+    fill(at);
+    sc_next = scales(at);
+  }
+
   // Q: row r = query * group + head-in-group; lane (g, t) holds channels
   // [64 j + 16 t, +16) of row 8 rg + g
-  uint32_t qf[KBLK][8];
+  uint32_t qh[KBLK][4], ql[KBLK][4];  // digits of 4 channels per word
+  float qs[2];                        // scales of rows 2t, 2t + 1
   {
     const int r = rg * 8 + g;
     const bool live = r < rows;
     const int qi = live ? r / a.group : 0, hl = live ? r - qi * a.group : 0;
-    const bf16* qp = a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head;
+    const bf16* qp = a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + 16 * t;
+    uint4 x[KBLK][2];
+    uint32_t am = 0;
 #pragma unroll
-    for (int j = 0; j < KBLK; ++j) {
-      uint4 x = make_uint4(0, 0, 0, 0), y = x;
-      if (live) {
-        x = *reinterpret_cast<const uint4*>(qp + 64 * j + 16 * t);
-        y = *reinterpret_cast<const uint4*>(qp + 64 * j + 16 * t + 8);
+    for (int j = 0; j < KBLK; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[j][i] = live ? *reinterpret_cast<const uint4*>(qp + 64 * j + 8 * i) : make_uint4(0, 0, 0, 0);
+        am = __vmaxu2(am, __vmaxu2(__vmaxu2(x[j][i].x & 0x7FFF7FFFu, x[j][i].y & 0x7FFF7FFFu),
+                                   __vmaxu2(x[j][i].z & 0x7FFF7FFFu, x[j][i].w & 0x7FFF7FFFu)));
       }
-      qf[j][0] = x.x; qf[j][1] = x.y; qf[j][2] = x.z; qf[j][3] = x.w;
-      qf[j][4] = y.x; qf[j][5] = y.y; qf[j][6] = y.z; qf[j][7] = y.w;
-    }
+    am = max(am << 16, am & 0xFFFF0000u);
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+    // rows below 2^-110 count as zeros; a NaN or an infinity makes every score NaN
+    const bool some = am >= 0x08800000u && am < 0x7F800000u;
+    const float amax = __uint_as_float(am);
+    const float inv = some ? 32639.f / amax : 0.f;  // 127 * 256 + 127
+    const float sc = am >= 0x7F800000u ? __int_as_float(0x7FC00000) : some ? amax * (1.f / 32639.f) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) qs[i] = __shfl_sync(0xFFFFFFFFu, sc, (2 * t + i) * 4) * a.scale_log2;
+#pragma unroll
+    for (int j = 0; j < KBLK; ++j)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t src[2] = {(w & 1) ? x[j][w >> 1].z : x[j][w >> 1].x, (w & 1) ? x[j][w >> 1].w : x[j][w >> 1].y};
+        uint32_t hi = 0, lo = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = __uint_as_float((i & 1) ? src[i >> 1] & 0xFFFF0000u : src[i >> 1] << 16);
+          const int v = some ? __float2int_rn(f * inv) : 0;
+          const int d = (v + 128) >> 8;
+          hi |= (uint32_t)(d & 0xFF) << (8 * i);
+          lo |= (uint32_t)((v - (d << 8)) & 0xFF) << (8 * i);
+        }
+        qh[j][w] = hi;
+        ql[j][w] = lo;
+      }
   }
   // first key that rows 2t and 2t + 1 of the group cannot see
   int lim[2];
@@ -195,12 +283,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     const int r = rg * 8 + 2 * t + i;
     lim[i] = a.causal && r < rows ? min(len, len - a.n_q + 1 + r / a.group) : len;
   }
-
-  const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
-  const int8_t* kb = a.c.k + base * D;
-  const int8_t* vb = a.c.v + base * D;
-  const float* ksb = a.c.k_scale + base;
-  const float* vsb = a.c.v_scale + base;
 
   float o[VBLK][VM][4];
 #pragma unroll
@@ -211,66 +293,47 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       for (int j = 0; j < 4; ++j) o[i][m][j] = 0.f;
   float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
-  uint4 kr[2][KBLK];          // keys g, g + 8
-  uint32_t vr[4][VBLK][VB / 4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-  float ks[2], vs[2];
-  auto load_k = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int key = min(at + g + 8 * i, key1 - 1);  // past the range: a key of it, masked below
-      ks[i] = __ldg(ksb + key);
-      vs[i] = __ldg(vsb + key);
-#pragma unroll
-      for (int j = 0; j < KBLK; ++j)
-        kr[i][j] = __ldg(reinterpret_cast<const uint4*>(kb + (size_t)key * D + 64 * j + 16 * t));
-    }
-  };
-  auto load_v = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int key = min(at + 2 * t + (i & 1) + (i >> 1) * 8, key1 - 1);
-#pragma unroll
-      for (int j = 0; j < VBLK; ++j) {
-        const int8_t* p = vb + (size_t)key * D + (8 * VB) * j + VB * g;
-        if constexpr (VB == 16) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(p));
-          vr[i][j][0] = x.x; vr[i][j][1] = x.y; vr[i][j][2] = x.z; vr[i][j][3] = x.w;
-        } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(p));
-          vr[i][j][0] = x.x; vr[i][j][1] = x.y;
-        }
-      }
-    }
-  };
-
-  int at = key0 + warp * kTileKeys;
-  if (at < key1) {
-    load_k(at);
-    load_v(at);
-  }
   for (; at < key1; at += STEP) {
+    const float sc = sc_next;
+    const int cur = tiles - 1;  // the tile at work; the next one is asked for now
+    if (at + STEP < key1) {
+      fill(at + STEP);
+      sc_next = scales(at + STEP);
+    }
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_bar[warp][cur % kStages], (cur / kStages) & 1, a.err.wait_ns))) {
+      set_error(a.err, DEV_TIMEOUT);
+      for (int i = cur; i < tiles; ++i)  // copies still in flight must land before their stage is used again
+        if (!mbar_wait(&s_bar[warp][i % kStages], (i / kStages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
+      break;
+    }
+    const int8_t* tile = ring + (cur % kStages) * few_stage(D);
     // scores of 16 keys x 8 rows: lane holds keys g, g + 8, rows 2t, 2t + 1
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    int ch[4] = {0, 0, 0, 0}, cl[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < KBLK; ++j) {
-      const uint32_t w0[4] = {kr[0][j].x, kr[0][j].y, kr[0][j].z, kr[0][j].w};
-      const uint32_t w1[4] = {kr[1][j].x, kr[1][j].y, kr[1][j].z, kr[1][j].w};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        const uint32_t f[4] = {bytes_bf16x2(__byte_perm(w0[s], 0, 0x4140)), bytes_bf16x2(__byte_perm(w1[s], 0, 0x4140)),
-                               bytes_bf16x2(__byte_perm(w0[s], 0, 0x4342)), bytes_bf16x2(__byte_perm(w1[s], 0, 0x4342))};
-        mma_bf16(c, f, qf[j][2 * s], qf[j][2 * s + 1]);
-      }
+      const uint4 x0 = *reinterpret_cast<const uint4*>(tile + g * D + 64 * j + 16 * t);
+      const uint4 x1 = *reinterpret_cast<const uint4*>(tile + (g + 8) * D + 64 * j + 16 * t);
+      mma_s8(ch, x0.x, x1.x, x0.y, x1.y, qh[j][0], qh[j][1]);
+      mma_s8(cl, x0.x, x1.x, x0.y, x1.y, ql[j][0], ql[j][1]);
+      mma_s8(ch, x0.z, x1.z, x0.w, x1.w, qh[j][2], qh[j][3]);
+      mma_s8(cl, x0.z, x1.z, x0.w, x1.w, ql[j][2], ql[j][3]);
     }
-    const float k0 = ks[0] * a.scale_log2, k1 = ks[1] * a.scale_log2;
+    float ks[2], vs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ks[i] = __shfl_sync(0xFFFFFFFFu, sc, g + 8 * i);
+      vs[i] = __shfl_sync(0xFFFFFFFFu, sc, 16 + g + 8 * i);
+    }
+    float c[4];  // (|256 hi + lo| < 2^31: 127 * 127 * 256 * 257)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = (float)(ch[i] * 256 + cl[i]) * qs[i & 1];
     const float v0 = vs[0], v1 = vs[1];
-    if (at + STEP < key1) load_k(at + STEP);  // the next tile's keys under this one's softmax
     const int ka = at + g, kc = ka + 8;
     float x[4];
-    x[0] = ka < min(lim[0], key1) ? c[0] * k0 : -INFINITY;
-    x[1] = ka < min(lim[1], key1) ? c[1] * k0 : -INFINITY;
-    x[2] = kc < min(lim[0], key1) ? c[2] * k1 : -INFINITY;
-    x[3] = kc < min(lim[1], key1) ? c[3] * k1 : -INFINITY;
+    x[0] = ka < min(lim[0], key1) ? c[0] * ks[0] : -INFINITY;
+    x[1] = ka < min(lim[1], key1) ? c[1] * ks[0] : -INFINITY;
+    x[2] = kc < min(lim[0], key1) ? c[2] * ks[1] : -INFINITY;
+    x[3] = kc < min(lim[1], key1) ? c[3] * ks[1] : -INFINITY;
     float al[2];
     bool grow = false;
 #pragma unroll
@@ -308,18 +371,31 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     for (int i = 0; i < 4; ++i) p[i] = x[i] == -INFINITY ? 0.f : p[i] * (i < 2 ? v0 : v1);
     const uint32_t b0 = movmatrix(pack_bf16(p[0], p[1])), b1 = movmatrix(pack_bf16(p[2], p[3]));
 #pragma unroll
-    for (int j = 0; j < VBLK; ++j)
+    for (int j = 0; j < VBLK; ++j) {
+      uint32_t vr[4][VB / 4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int8_t* p8 = tile + (kTileKeys + 2 * t + (i & 1) + (i >> 1) * 8) * D + (8 * VB) * j + VB * g;
+        if constexpr (VB == 16) {
+          const uint4 x4 = *reinterpret_cast<const uint4*>(p8);
+          vr[i][0] = x4.x; vr[i][1] = x4.y; vr[i][2] = x4.z; vr[i][3] = x4.w;
+        } else {
+          const uint2 x2 = *reinterpret_cast<const uint2*>(p8);
+          vr[i][0] = x2.x; vr[i][1] = x2.y;
+        }
+      }
 #pragma unroll
       for (int m = 0; m < VM; ++m) {
         const int w = m >> 1;
         const uint32_t lo = (m & 1) ? 0x0602u : 0x0400u, hi = (m & 1) ? 0x0703u : 0x0501u;
-        const uint32_t f[4] = {bytes_bf16x2(__byte_perm(vr[0][j][w], vr[1][j][w], lo)),
-                               bytes_bf16x2(__byte_perm(vr[0][j][w], vr[1][j][w], hi)),
-                               bytes_bf16x2(__byte_perm(vr[2][j][w], vr[3][j][w], lo)),
-                               bytes_bf16x2(__byte_perm(vr[2][j][w], vr[3][j][w], hi))};
+        const uint32_t f[4] = {bytes_bf16x2(__byte_perm(vr[0][w], vr[1][w], lo)),
+                               bytes_bf16x2(__byte_perm(vr[0][w], vr[1][w], hi)),
+                               bytes_bf16x2(__byte_perm(vr[2][w], vr[3][w], lo)),
+                               bytes_bf16x2(__byte_perm(vr[2][w], vr[3][w], hi))};
         mma_bf16(o[j][m], f, b0, b1);
       }
-    if (at + STEP < key1) load_v(at + STEP);
+    }
+    __syncwarp();  // every lane has read the stage: the next copy may overwrite it
   }
 
   // row sums over the 8 lanes that share t
@@ -398,7 +474,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     b_unit = unit;
     ++b;
   }
-  __syncthreads();  // s_o and the statistics are free again
+  fence_proxy_async_smem();  // s_o was written by threads, the rings are written by copies
+  __syncthreads();           // s_o and the statistics are free again
   }
 }
 
@@ -538,7 +615,7 @@ __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int spli
   }
 }
 
-size_t few_smem(int d) { return (size_t)kWarps * 8 * (d + 4) * 4; }
+size_t few_smem(int d) { return (size_t)kWarps * kStages * few_stage(d); }  // (covers [kWarps][8][d + 4] floats)
 
 template <int D>
 cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st) {
@@ -569,10 +646,10 @@ Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new
   const int keys = std::max(1, max_keys + n_new);
   int splits = 1;
   if (!p.tc) {
-    // blocks that deal out the units of 64 keys: two (four for head_dim < 256)
+    // blocks that deal out the units of 64 keys: three (four for head_dim < 256)
     // resident per SM, and no more than there are units in a full cache
     const long long units = blocks * ((std::max(max_keys, 1) - 1) / kUnit + 1);
-    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
+    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 3 : 4));
     // (with one unit per item no item is shared)
     p.ws_bytes = p.splits > 1 && units > blocks ? (size_t)p.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
     return p;
@@ -585,6 +662,8 @@ Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new
 
 cudaError_t kv8_attn_init() {
   cudaError_t e = cudaFuncSetAttribute(k_kv8_attn_few<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(256));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv8_attn_few<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(128));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(k_kv8_attn_few<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem(64));
   return e == cudaSuccess ? kv8_attn_tc_init() : e;
 }
 
