@@ -100,6 +100,11 @@ constexpr int kUnit = kWarps * kTileKeys;
 __device__ __forceinline__ int seq_len(const Kv8AttnArgs& a, int b) { return max(0, min(__ldg(a.lens + b), a.c.cap)); }
 __device__ __forceinline__ int seq_units(int len) { return len < 1 ? 1 : (len - 1) / kUnit + 1; }
 
+// a / b for a >= 0, b > 0: in 32 bits where they suffice
+__device__ __forceinline__ long long div_ll(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // Exclusive prefix sums of the sequences' units over the block: thread i holds
 // a slice [b0, b1) and gets the units before it; returns the total.  `sh` has
 // NT / 32 entries.
@@ -142,7 +147,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 }
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(const Kv8AttnArgs a, int rgs) {
+__global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(const Kv8AttnArgs a, int rgs) {
   constexpr int KBLK = D / 64;               // 64-channel blocks of a K row
   constexpr int VB = D >= 128 ? 16 : 8;      // bytes of a V row per lane and block
   constexpr int VBLK = D / (8 * VB);         // blocks of a V row
@@ -163,8 +168,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
     for (int i = 0; i < kStages; ++i) mbar_init(&s_bar[warp][i], 1);
     fence_mbar_init();
   }
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();  // after the wait: the merge may read the lengths before its own
 
   // this block's units, and the sequence the first of them lies in
   long long unit, unit_end;
@@ -176,8 +181,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
     const long long total = scan_units<kWarps * 32>(a, s_scan, b0, b1, before) * hr;
     const long long G = min((long long)gridDim.x, total);  // blocks with units
     if (blockIdx.x >= G) return;
-    unit = total * blockIdx.x / G;
-    unit_end = total * (blockIdx.x + 1) / G;
+    unit = div_ll(total * blockIdx.x, G);
+    unit_end = div_ll(total * (blockIdx.x + 1), G);
     before *= hr;
     for (int i = b0; i < b1; ++i) {
       const long long n = (long long)seq_units(seq_len(a, i)) * hr;
@@ -195,10 +200,26 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
   int tiles = 0;  // tiles this warp has asked for: tile i goes through stage i % kStages
   while (unit < unit_end) {
   const int len = seq_len(a, b), units = seq_units(len);
-  const int item = (int)((unit - b_unit) / units), u0 = (int)((unit - b_unit) - (long long)item * units);
+  const int item = (int)div_ll(unit - b_unit, units), u0 = (int)((unit - b_unit) - (long long)item * units);
   const int u1 = (int)min((long long)units, u0 + (unit_end - unit));
   const int h = item / rgs, rg = item - h * rgs;
   const int key0 = min(len, u0 * STEP), key1 = (int)min((long long)len, (long long)u1 * STEP);
+
+  // Q: row r = query * group + head-in-group; lane (g, t) holds channels
+  // [64 j + 16 t, +16) of row 8 rg + g (asked for before the key tiles, which
+  // would keep it waiting)
+  uint4 x[KBLK][2];
+  {
+    const int r = rg * 8 + g;
+    const bool live = r < rows;
+    const int qi = live ? r / a.group : 0, hl = live ? r - qi * a.group : 0;
+    const bf16* qp = a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + 16 * t;
+#pragma unroll
+    for (int j = 0; j < KBLK; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[j][i] = live ? __ldg(reinterpret_cast<const uint4*>(qp + 64 * j + 8 * i)) : make_uint4(0, 0, 0, 0);
+  }
 
   const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
   // Each warp streams its own tiles through a ring of its own: one bulk copy
@@ -223,28 +244,23 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
     return __ldg((lane < 16 ? a.c.k_scale : a.c.v_scale) + base + key);
   };
   int at = key0 + warp * kTileKeys;
-  float sc_next = 0.f;
-  if (at < key1) {
-    fill(at);
-    sc_next = scales(at);
-  }
+  float sc_next[kStages];
+  int cur = tiles;  // the tile at work
+#pragma unroll
+  for (int i = 0; i < kStages; ++i)
+    if (at + i * STEP < key1) {
+      fill(at + i * STEP);
+      sc_next[i] = scales(at + i * STEP);
+    }
 
-  // Q: row r = query * group + head-in-group; lane (g, t) holds channels
-  // [64 j + 16 t, +16) of row 8 rg + g
   uint32_t qh[KBLK][4], ql[KBLK][4];  // digits of 4 channels per word
   float qs[2];                        // scales of rows 2t, 2t + 1
   {
-    const int r = rg * 8 + g;
-    const bool live = r < rows;
-    const int qi = live ? r / a.group : 0, hl = live ? r - qi * a.group : 0;
-    const bf16* qp = a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + 16 * t;
-    uint4 x[KBLK][2];
     uint32_t am = 0;
 #pragma unroll
     for (int j = 0; j < KBLK; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[j][i] = live ? *reinterpret_cast<const uint4*>(qp + 64 * j + 8 * i) : make_uint4(0, 0, 0, 0);
         am = __vmaxu2(am, __vmaxu2(__vmaxu2(x[j][i].x & 0x7FFF7FFFu, x[j][i].y & 0x7FFF7FFFu),
                                    __vmaxu2(x[j][i].z & 0x7FFF7FFFu, x[j][i].w & 0x7FFF7FFFu)));
       }
@@ -258,22 +274,20 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
     const float sc = am >= 0x7F800000u ? __int_as_float(0x7FC00000) : some ? amax * (1.f / 32639.f) : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) qs[i] = __shfl_sync(0xFFFFFFFFu, sc, (2 * t + i) * 4) * a.scale_log2;
+    // q inv + (1.5 2^23 + 128) rounds to a whole number in the low bits of the
+    // sum: byte 1 is hi, byte 0 is lo + 128
 #pragma unroll
     for (int j = 0; j < KBLK; ++j)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const uint32_t src[2] = {(w & 1) ? x[j][w >> 1].z : x[j][w >> 1].x, (w & 1) ? x[j][w >> 1].w : x[j][w >> 1].y};
-        uint32_t hi = 0, lo = 0;
+        const uint32_t s0 = (w & 1) ? x[j][w >> 1].z : x[j][w >> 1].x, s1 = (w & 1) ? x[j][w >> 1].w : x[j][w >> 1].y;
+        const float f[4] = {__uint_as_float(s0 << 16), __uint_as_float(s0 & 0xFFFF0000u), __uint_as_float(s1 << 16),
+                            __uint_as_float(s1 & 0xFFFF0000u)};
+        uint32_t m[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = __uint_as_float((i & 1) ? src[i >> 1] & 0xFFFF0000u : src[i >> 1] << 16);
-          const int v = some ? __float2int_rn(f * inv) : 0;
-          const int d = (v + 128) >> 8;
-          hi |= (uint32_t)(d & 0xFF) << (8 * i);
-          lo |= (uint32_t)((v - (d << 8)) & 0xFF) << (8 * i);
-        }
-        qh[j][w] = hi;
-        ql[j][w] = lo;
+        for (int i = 0; i < 4; ++i) m[i] = some ? __float_as_uint(fmaf(f[i], inv, 12583040.f)) : 0x80u;
+        qh[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0051), __byte_perm(m[2], m[3], 0x0051), 0x5410);
+        ql[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410) ^ 0x80808080u;
       }
   }
   // first key that rows 2t and 2t + 1 of the group cannot see
@@ -294,12 +308,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
   float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 
   for (; at < key1; at += STEP) {
-    const float sc = sc_next;
-    const int cur = tiles - 1;  // the tile at work; the next one is asked for now
-    if (at + STEP < key1) {
-      fill(at + STEP);
-      sc_next = scales(at + STEP);
-    }
+    const float sc = sc_next[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) sc_next[i] = sc_next[i + 1];
     if (!__all_sync(0xFFFFFFFFu, mbar_wait(&s_bar[warp][cur % kStages], (cur / kStages) & 1, a.err.wait_ns))) {
       set_error(a.err, DEV_TIMEOUT);
       for (int i = cur; i < tiles; ++i)  // copies still in flight must land before their stage is used again
@@ -396,6 +407,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
       }
     }
     __syncwarp();  // every lane has read the stage: the next copy may overwrite it
+    if (at + kStages * STEP < key1) {
+      fill(at + kStages * STEP);
+      sc_next[kStages - 1] = scales(at + kStages * STEP);
+    }
+    ++cur;
   }
 
   // row sums over the 8 lanes that share t
@@ -479,6 +495,19 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 3 : 4) k_kv8_attn_few(
   }
 }
 
+// (m, l, acc) joined with the row x of maximum and sum ml; no maximum: nothing
+// was visible there, and x is passed over.
+__device__ __forceinline__ void merge_part(float2 ml, float4 x, float& m, float& l, float4& acc) {
+  if (ml.x == -INFINITY) return;
+  const float nm = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2(m - nm), w = ex2(ml.x - nm);
+  m = nm;
+  l = fmaf(l, f, w * ml.y);
+  acc.x = fmaf(acc.x, f, w * x.x);
+  acc.y = fmaf(acc.y, f, w * x.y);
+  acc.z = fmaf(acc.z, f, w * x.z);
+  acc.w = fmaf(acc.w, f, w * x.w);
+}
+
 // Joins the parts of the (sequence, KV head, row group) items that
 // k_kv8_attn_few left to several blocks: one block per (row, item).
 template <int D>
@@ -486,15 +515,16 @@ __global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int 
   constexpr int C4 = D / 4, NS = 256 / C4;
   __shared__ long long s_scan[8];
   __shared__ long long s_before;
-  __shared__ float s_red[32];
+  __shared__ float2 s_ml[NS];
   __shared__ float4 s_acc[256];
-  pdl_launch_dependents();
-  pdl_wait();
   const int item_all = blockIdx.x, r = blockIdx.y;  // ((sequence, KV head), row group); row of the group
   const int hr = a.c.heads * rgs, b = item_all / hr, item = item_all - b * hr;
   const int h = item / rgs, rg = item - h * rgs;
   const int row = rg * 8 + r;
+  pdl_launch_dependents();
   if (row >= a.group * a.n_q) return;
+  // which blocks hold the item: only the lengths are needed, which no kernel
+  // in flight writes (the attention let this one start after its own wait)
   const int units = seq_units(seq_len(a, b));
   long long total;
   {
@@ -510,50 +540,33 @@ __global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int 
   const long long first = s_before * hr + (long long)item * units, last = first + units - 1;
   // block i of G holds units [total i / G, total (i + 1) / G)
   const long long G = min((long long)blocks, total);
-  const int c0 = (int)(((first + 1) * G - 1) / total), c1 = (int)(((last + 1) * G - 1) / total);
+  const int c0 = (int)div_ll((first + 1) * G - 1, total), c1 = (int)div_ll((last + 1) * G - 1, total);
+  pdl_wait();
   if (c0 == c1) return;  // written by its one block
   const int tid = threadIdx.x;
-  auto slot = [&](int c) -> size_t {  // the item begins in c0 only
-    return ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 8 + r;
-  };
-  float M = -INFINITY;
-  for (int c = c0 + tid; c <= c1; c += 256) M = fmaxf(M, __ldcg(&a.part_ml[slot(c)].x));
-  M = warp_max(M);
-  if ((tid & 31) == 0) s_red[tid >> 5] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_red[w]);
-  float l = 0.f;
   const int c4 = tid % C4, part = tid / C4;
+  // every NS-th part, its running maximum and sums as in the attention
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0 + part; c <= c1; c += NS) {
-    const size_t pr = slot(c);
-    const float2 ml = __ldcg(a.part_ml + pr);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c4));
-    if (ml.x == -INFINITY) continue;  // no visible key in this part
-    const float w = ex2(ml.x - M);
-    l = fmaf(w, ml.y, l);
-    acc.x = fmaf(w, x.x, acc.x);
-    acc.y = fmaf(w, x.y, acc.y);
-    acc.z = fmaf(w, x.z, acc.z);
-    acc.w = fmaf(w, x.w, acc.w);
+  for (int cb = c0 + part; cb <= c1; cb += 4 * NS) {
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // four parts in flight
+      const int c = cb + i * NS;
+      const size_t pr = ((size_t)c * 2 + (c == c0 ? 1 : 0)) * 8 + r;  // the item begins in c0 only
+      ml[i] = c <= c1 ? __ldcg(a.part_ml + pr) : make_float2(-INFINITY, 0.f);
+      x[i] = c <= c1 ? __ldcg(reinterpret_cast<const float4*>(a.part_o + pr * D + 4 * c4)) : acc;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) merge_part(ml[i], x[i], m, l, acc);
   }
   s_acc[tid] = acc;
-  __syncthreads();
-  if (c4 == 0) s_red[part] = l;
+  if (c4 == 0) s_ml[part] = make_float2(m, l);
   __syncthreads();
   if (part == 0) {
-    l = 0.f;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) l += s_red[s];
-#pragma unroll
-    for (int s = 1; s < NS; ++s) {
-      const float4 x = s_acc[s * C4 + c4];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
-    }
+    for (int s = 1; s < NS; ++s) merge_part(s_ml[s], s_acc[s * C4 + c4], m, l, acc);
     const int qi = row / a.group, hl = row - qi * a.group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
@@ -562,57 +575,33 @@ __global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int 
 }
 
 // The parts of k_kv8_attn_tc: o = sum_s w_s O_s / sum_s w_s l_s with w_s =
-// 2^(m_s - max m); one block per (sequence, KV head, row).  Splits without a visible key (m = -inf) wrote no
-// row and are passed over.
+
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int splits, int rowsp) {
-  constexpr int C4 = D / 4, NS = 256 / C4;
-  __shared__ float s_w[kMaxKv8Splits];
-  __shared__ float s_red[8];
-  __shared__ float4 s_acc[256];
+  constexpr int C4 = D / 4, NR = 256 / C4;  // rows per block
+  const int row = blockIdx.x * NR + threadIdx.x / C4, c4 = threadIdx.x % C4, bg = blockIdx.y;
   pdl_launch_dependents();
   pdl_wait();
-  const int row = blockIdx.x, bg = blockIdx.y;
+  if (row >= a.group * a.n_q) return;
   const int b = bg / a.c.heads, h = bg - b * a.c.heads;
   const size_t p0 = (size_t)bg * splits * rowsp + row;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  float2 ml = make_float2(-INFINITY, 0.f);
-  if (tid < splits) ml = __ldcg(a.part_ml + p0 + (size_t)tid * rowsp);
-  float M = warp_max(ml.x);
-  if (lane == 0) s_red[warp] = M;
-  __syncthreads();
+  float2 ml[kMaxKv8Splits];
+  float4 x[kMaxKv8Splits];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) M = fmaxf(M, s_red[w]);
-  const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-  if (tid < splits) s_w[tid] = w;
-  const float l = block_sum(ml.x == -INFINITY ? 0.f : w * ml.y, s_red);  // (its barriers also order s_w)
-  const int c4 = tid % C4, part = tid / C4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = part; s < splits; s += NS) {
-    const float ws = s_w[s];
-    if (ws == 0.f) continue;
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p0 + (size_t)s * rowsp) * D + 4 * c4));
-    acc.x = fmaf(ws, x.x, acc.x);
-    acc.y = fmaf(ws, x.y, acc.y);
-    acc.z = fmaf(ws, x.z, acc.z);
-    acc.w = fmaf(ws, x.w, acc.w);
-  }
-  s_acc[tid] = acc;
-  __syncthreads();
-  if (part == 0) {
-#pragma unroll
-    for (int s = 1; s < NS; ++s) {
-      const float4 x = s_acc[s * C4 + c4];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
+  for (int s = 0; s < kMaxKv8Splits; ++s)
+    if (s < splits) {
+      ml[s] = __ldcg(a.part_ml + p0 + (size_t)s * rowsp);
+      x[s] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p0 + (size_t)s * rowsp) * D + 4 * c4));
     }
-    const int qi = row / a.group, hl = row - qi * a.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
-    *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  }
+  float m = -INFINITY, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int s = 0; s < kMaxKv8Splits; ++s)
+    if (s < splits) merge_part(ml[s], x[s], m, l, acc);
+  const int qi = row / a.group, hl = row - qi * a.group;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
+  *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }
 
 size_t few_smem(int d) { return (size_t)kWarps * kStages * few_stage(d); }  // (covers [kWarps][8][d + 4] floats)
@@ -626,7 +615,8 @@ cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cud
 }
 template <int D>
 cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {  // (PDL behind its own attention)
-  return launch_ex(k_kv8_merge<D>, dim3(a.group * a.n_q, a.n_seq * a.c.heads), dim3(256), 0, st, 1, true, a, p.splits,
+  const int nr = 1024 / D;  // rows per block
+  return launch_ex(k_kv8_merge<D>, dim3((a.group * a.n_q + nr - 1) / nr, a.n_seq * a.c.heads), dim3(256), 0, st, 1, true, a, p.splits,
                    p.qtiles * (p.tc ? 128 : 8));
 }
 
@@ -646,10 +636,10 @@ Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new
   const int keys = std::max(1, max_keys + n_new);
   int splits = 1;
   if (!p.tc) {
-    // blocks that deal out the units of 64 keys: three (four for head_dim < 256)
+    // blocks that deal out the units of 64 keys: two (four for head_dim < 256)
     // resident per SM, and no more than there are units in a full cache
     const long long units = blocks * ((std::max(max_keys, 1) - 1) / kUnit + 1);
-    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 3 : 4));
+    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
     // (with one unit per item no item is shared)
     p.ws_bytes = p.splits > 1 && units > blocks ? (size_t)p.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
     return p;

@@ -4,7 +4,8 @@
 // 127 (rounded once to fp32), so x_i is read back as q_i s, off by at most
 // s / 2.  The code is that of the exact quotient, ties to even: x_i (1/s) in
 // fp32 can land on the wrong side of a half, so near one the sign of
-// x_i - (n + 1/2) s decides, which one fused multiply-add gives exactly.
+// x_i - (n + 1/2) s decides, which one fused multiply-add gives exactly.  Few
+// values are that near; the others cost five instructions each.
 // s below 2^-120 is taken as 0 (codes 0): above it 1/s, the products and that
 // sign are free of overflow and underflow.  A row with a NaN or an infinity
 // gets scale NaN and codes 0: it reads back as NaN and says so.
@@ -25,21 +26,23 @@ namespace {
 
 constexpr float kTinyScale = 7.52316384526264e-37f;  // 2^-120
 
-// Scale of a row from the bits of its largest |x| (as an integer maximum: NaN
-// and infinity sort above every finite value).
+// Scale of a row from the bits of its largest |x| (NaN and infinity sort above
+// every finite value).
 __device__ __forceinline__ float row_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return __int_as_float(0x7FC00000);
   const float s = __fdiv_rn(__uint_as_float(amax_bits), 127.f);
   return s < kTinyScale ? 0.f : s;
 }
+__device__ __forceinline__ float inv_scale(float s) { return s > 0.f ? __fdiv_rn(1.f, s) : 0.f; }
 
-// rint(x / s) for |x| <= 127 s (1 + 2^-23), inv = 1 / s (0 when s is 0 or NaN)
+// rint(x / s) for |x| <= 127 s (1 + 2^-23), inv = 1 / s > 0.  t = x inv is off
+// by at most 127 * 2^-22: within 1e-4 of a half, floor(t) is the lower
+// neighbour of the exact quotient, and the fused product has the sign of the
+// quotient's difference from the half.
 __device__ __forceinline__ int quant1(float x, float s, float inv) {
   const float t = x * inv;
   float q = rintf(t);
   if (fabsf(t - q) > 0.4999f) {
-    // within 1e-4 of a half: t is off by at most 127 * 2^-22, so floor(t) is
-    // the lower neighbour, and the fused product has the difference's sign
     const float lo = floorf(t);
     const float e = __fmaf_rn(-(lo + 0.5f), s, x);
     q = e > 0.f ? lo + 1.f : e < 0.f ? lo : rintf(lo + 0.5f);
@@ -51,18 +54,31 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
   return (uint32_t)(a & 0xFF) | ((uint32_t)(b & 0xFF) << 8) | ((uint32_t)(c & 0xFF) << 16) | ((uint32_t)d << 24);
 }
 
-// 8 consecutive elements of a row in registers.
+// Largest magnitude of three; NaN if one of them is.
+__device__ __forceinline__ float amax3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// 8 elements of a row in registers, lane i of a row: bf16 elements [8 i, +8);
+// fp32 elements [4 i, +4) and [half + 4 i, +4), so that every 16-byte access of
+// neighbouring lanes is one contiguous run.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<bf16> {
   uint4 w;
-  __device__ __forceinline__ void load(const bf16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void load(const bf16* row, int lane, int) { w = reinterpret_cast<const uint4*>(row)[lane]; }
+  static __device__ __forceinline__ void put_codes(int8_t* row, int lane, int, uint2 q) { reinterpret_cast<uint2*>(row)[lane] = q; }
+  static __device__ __forceinline__ uint2 get_codes(const int8_t* row, int lane, int) { return reinterpret_cast<const uint2*>(row)[lane]; }
   __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  // the bits of the largest |x|, as fp32
   __device__ __forceinline__ uint32_t amax() const {
-    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-    return max(m << 16, m & 0xFFFF0000u);
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3])));
+    const uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+    return max(u << 16, u & 0xFFFF0000u);
   }
   __device__ __forceinline__ void get(float* f) const {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -75,35 +91,55 @@ struct Vec8<bf16> {
 };
 template <>
 struct Vec8<float> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const uint4*>(p)[0];
-    b = reinterpret_cast<const uint4*>(p)[1];
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* row, int lane, int half) {
+    a = reinterpret_cast<const float4*>(row)[lane];
+    b = reinterpret_cast<const float4*>(row + half)[lane];
   }
-  __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
+  static __device__ __forceinline__ void put_codes(int8_t* row, int lane, int half, uint2 q) {
+    reinterpret_cast<uint32_t*>(row)[lane] = q.x;
+    reinterpret_cast<uint32_t*>(row + half)[lane] = q.y;
+  }
+  static __device__ __forceinline__ uint2 get_codes(const int8_t* row, int lane, int half) {
+    return make_uint2(reinterpret_cast<const uint32_t*>(row)[lane], reinterpret_cast<const uint32_t*>(row + half)[lane]);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void put(const float* f) {
-    a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-    b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
   }
   __device__ __forceinline__ uint32_t amax() const {
-    const uint32_t k = 0x7FFFFFFFu;
-    return max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)), max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
+    return __float_as_uint(amax3(amax3(amax3(a.x, a.y, a.z), a.w, b.x), amax3(b.y, b.z, b.w), 0.f));
   }
   __device__ __forceinline__ void get(float* f) const {
-    const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
 };
 
+// 8 codes.  x inv + 1.5 2^23 rounds to a whole number in the low bits of the
+// sum (the codes are its low bytes); the residual x - q s tells whether the
+// rounding can be wrong, which only values within 1e-6 of a half are, and
+// those go through quant1.
 __device__ __forceinline__ uint2 quant8(const float* f, float s, float inv) {
-  int q[8];
+  constexpr float kMagic = 12582912.f;
+  uint32_t m[8];
+  float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = quant1(f[i], s, inv);
-  return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+  for (int i = 0; i < 8; ++i) {
+    const float r = fmaf(f[i], inv, kMagic);
+    m[i] = __float_as_uint(r);
+    worst = fmaxf(worst, fabsf(fmaf(kMagic - r, s, f[i])));
+  }
+  if (worst > s * 0.499999f) {
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = quant1(f[i], s, inv);
+    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+  }
+  return make_uint2(__byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410),
+                    __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410));
 }
-
-__device__ __forceinline__ float inv_scale(float s) { return s > 0.f ? __fdiv_rn(1.f, s) : 0.f; }
 
 // s / sqrt(mean x^2 + eps).  Squares of rows with s >= 1 are taken in units of
 // s (they cannot overflow), others as they are (eps / s^2 cannot).
@@ -134,7 +170,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
   for (int i = 0; i < NV; ++i) {
     const int c = lane + i * TPR;
     if (live && c < nv)
-      v[i].load(xr + (size_t)c * 8);
+      v[i].load(xr, c, width / 2);
     else
       v[i].zero();
   }
@@ -151,7 +187,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
   const float s = row_scale(am);
   const float inv = inv_scale(s);
   const float unit = rms_unit(s, inv);
-  uint2* cr = reinterpret_cast<uint2*>(codes + (size_t)row * width);
+  int8_t* cr = codes + (size_t)row * width;
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -159,7 +195,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
     if (live && c < nv) {
       float f[8];
       v[i].get(f);
-      cr[c] = inv > 0.f ? quant8(f, s, inv) : make_uint2(0, 0);
+      Vec8<T>::put_codes(cr, c, width / 2, inv > 0.f ? quant8(f, s, inv) : make_uint2(0, 0));
       if (rms_eps > 0.f) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -253,166 +289,175 @@ cudaError_t quant_sel(const void* x, long long ldx, int rows, int width, float e
 // Slot and position of packed row t: sequence b = the last with cu[b] <= t
 // (binary search; empty sequences have cu[b] == cu[b + 1] and are passed
 // over).  Rows outside every sequence, and rows that would fall outside the
-// slot, have no place.
-__device__ __forceinline__ bool kv8_place(const Kv8Rows& r, int cap, int t, int& slot, int& pos) {
+// slot, have no place.  The offsets of up to kPlaceSeqs sequences are searched
+// in shared memory: a search in global memory is a chain of L2 round trips
+// (writing one row for each of 32 sequences took 5.5 us with it).
+constexpr int kPlaceSeqs = 1024;
+struct PlaceSmem {
+  int cu[kPlaceSeqs + 1], start[kPlaceSeqs];
+};
+__device__ __forceinline__ void place_load(const Kv8Rows& r, PlaceSmem& p) {  // a barrier must follow
+  if (!r.cu || r.n_seq > kPlaceSeqs) return;
+  for (int i = threadIdx.x; i <= r.n_seq; i += 256) p.cu[i] = __ldg(r.cu + i);
+  for (int i = threadIdx.x; i < r.n_seq; i += 256) p.start[i] = r.start ? __ldg(r.start + i) : 0;
+}
+__device__ __forceinline__ bool kv8_place(const Kv8Rows& r, const PlaceSmem& p, int cap, int t, int& slot, int& pos) {
   int b = 0;
   long long at = t;
   if (r.cu) {
-    if (r.n_seq < 1 || t < __ldg(r.cu) || t >= __ldg(r.cu + r.n_seq)) return false;
+    const bool sh = r.n_seq <= kPlaceSeqs;
+    const int* cu = sh ? p.cu : r.cu;
+    if (r.n_seq < 1 || t < cu[0] || t >= cu[r.n_seq]) return false;
     int lo = 0, hi = r.n_seq;  // cu[lo] <= t < cu[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(r.cu + mid) <= t)
+      if (cu[mid] <= t)
         lo = mid;
       else
         hi = mid;
     }
     b = lo;
-    at = (long long)t - __ldg(r.cu + b);
+    at = (long long)t - cu[b];
+    if (r.start) at += sh ? p.start[b] : __ldg(r.start + b);
+  } else if (r.start) {
+    at += __ldg(r.start);
   }
-  if (r.start) at += __ldg(r.start + b);
   slot = r.slot0 + b;
   pos = (int)at;
   return at >= 0 && at < cap;
 }
 
-// d / 8 lanes per row; a thread takes UNR (token, head) pairs, K and V of each
-// loaded before any is quantised.
+// blockIdx.y = KV head; d / 8 lanes per row, K and V of a token loaded before
+// either is quantised.
 template <typename T, int D, bool ROPE>
 __global__ void __launch_bounds__(256)
-    k_kv8_write(const Kv8 c, const Kv8Rows r, const Kv8Io io, const float2* __restrict__ rope_cs, long long items) {
-  constexpr int LPR = D / 8, UNR = 2;
+    k_kv8_write(const Kv8 c, const Kv8Rows r, const Kv8Io io, const float2* __restrict__ rope_cs) {
+  constexpr int LPR = D / 8, RPB = 256 / LPR;
+  __shared__ PlaceSmem place;
   pdl_launch_dependents();
   pdl_wait();
-  const int sub = threadIdx.x % LPR;
-  const long long gstep = (long long)gridDim.x * (256 / LPR);
-  const long long g0 = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
+  place_load(r, place);
+  const int sub = threadIdx.x % LPR, head = blockIdx.y;
+  const T* kp = static_cast<const T*>(io.k) + head * io.k_head;
+  const T* vp = static_cast<const T*>(io.v) + head * io.v_head;
+  bool placed = false;  // the offsets are in shared memory
   // whole warps stay in the loop together: the shuffles below need all lanes
-  const long long rounds = (items + gstep * UNR - 1) / (gstep * UNR);
-  for (long long rd = 0; rd < rounds; ++rd) {
-    Vec8<T> kv[UNR][2];
-    long long it[UNR];
-    int tok[UNR], head[UNR];
+  for (long long t0 = (long long)blockIdx.x * RPB; t0 < r.n_rows; t0 += (long long)gridDim.x * RPB) {
+    Vec8<T> kv[2];
+    const bool in = t0 + threadIdx.x / LPR < r.n_rows;
+    const int tok = (int)t0 + threadIdx.x / LPR;
+    if (in) {
+      kv[0].load(kp + tok * io.k_tok, sub, D / 2);
+      kv[1].load(vp + tok * io.v_tok, sub, D / 2);
+    } else {
+      kv[0].zero();
+      kv[1].zero();
+    }
+    if (!placed) __syncthreads();
+    placed = true;
+    int slot = 0, pos = 0;
+    const bool ok = in && kv8_place(r, place, c.cap, tok, slot, pos);
+    const size_t row = ((size_t)slot * c.heads + head) * c.cap + pos;
+    if constexpr (ROPE) {
+      // Rotate-half: channel i < d/2 pairs with i + d/2, which this lane holds
+      // too: a' = a cos - b sin, b' = b cos + a sin.
+      float f[8];
+      kv[0].get(f);
+      const float2* cs = rope_cs + (size_t)(ok ? pos : 0) * (D / 2) + sub * 4;
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      it[u] = g0 + (rd * UNR + u) * gstep;
-      if (it[u] < items) {
-        tok[u] = (int)(it[u] / c.heads);
-        head[u] = (int)(it[u] - (long long)tok[u] * c.heads);
-        kv[u][0].load(static_cast<const T*>(io.k) + tok[u] * io.k_tok + head[u] * io.k_head + sub * 8);
-        kv[u][1].load(static_cast<const T*>(io.v) + tok[u] * io.v_tok + head[u] * io.v_head + sub * 8);
-      } else {
-        kv[u][0].zero();
-        kv[u][1].zero();
+      for (int i = 0; i < 4; ++i) {
+        const float2 t = cs[i];
+        const float x = f[i], y = f[4 + i];
+        f[i] = x * t.x - y * t.y;
+        f[4 + i] = y * t.x + x * t.y;
       }
+      kv[0].put(f);
     }
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      int slot = 0, pos = 0;
-      const bool ok = it[u] < items && kv8_place(r, c.cap, tok[u], slot, pos);
-      const size_t row = ((size_t)slot * c.heads + (ok ? head[u] : 0)) * c.cap + pos;
-      if constexpr (ROPE) {
-        // Rotate-half: channel i < d/2 pairs with i + d/2, which the lane LPR/2
-        // away holds: a' = a cos - b sin, b' = b cos + a sin.
-        float f[8], g[8];
-        kv[u][0].get(f);
-        const bool hi = sub >= LPR / 2;
-        const float2* cs = rope_cs + (size_t)(ok ? pos : 0) * (D / 2) + (sub % (LPR / 2)) * 8;
+    for (int w = 0; w < 2; ++w) {
+      uint32_t am = kv[w].amax();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = __shfl_xor_sync(0xFFFFFFFFu, f[i], LPR / 2);
-          const float2 t = cs[i];
-          g[i] = hi ? f[i] * t.x + o * t.y : f[i] * t.x - o * t.y;
-        }
-        kv[u][0].put(g);
-      }
-#pragma unroll
-      for (int w = 0; w < 2; ++w) {
-        uint32_t am = kv[u][w].amax();
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-        const float s = row_scale(am);
-        const float inv = inv_scale(s);
-        if (ok) {
-          float f[8];
-          kv[u][w].get(f);
-          const uint2 q = inv > 0.f ? quant8(f, s, inv) : make_uint2(0, 0);
-          *reinterpret_cast<uint2*>((w ? c.v : c.k) + row * D + sub * 8) = q;
-          if (sub == 0) (w ? c.v_scale : c.k_scale)[row] = s;
-        }
+      for (int o = LPR / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+      const float s = row_scale(am);
+      const float inv = inv_scale(s);
+      if (ok) {
+        float f[8];
+        kv[w].get(f);
+        Vec8<T>::put_codes((w ? c.v : c.k) + row * D, sub, D / 2, inv > 0.f ? quant8(f, s, inv) : make_uint2(0, 0));
+        if (sub == 0) (w ? c.v_scale : c.k_scale)[row] = s;
       }
     }
   }
 }
 
-__device__ __forceinline__ float code_at(uint32_t w, int i) { return (float)(int)(int8_t)(w >> (8 * i)); }
-
-template <typename T>
-__device__ __forceinline__ void put8(T* p, const uint2 q, float s);
-template <>
-__device__ __forceinline__ void put8<float>(float* p, const uint2 q, float s) {
-  float4* d = reinterpret_cast<float4*>(p);
-  d[0] = make_float4(code_at(q.x, 0) * s, code_at(q.x, 1) * s, code_at(q.x, 2) * s, code_at(q.x, 3) * s);
-  d[1] = make_float4(code_at(q.y, 0) * s, code_at(q.y, 1) * s, code_at(q.y, 2) * s, code_at(q.y, 3) * s);
+// Codes of a word as fp32 times s: byte ^ 0x80 put into the low bits of 2^23
+// is 2^23 + 128 + code, exactly.
+__device__ __forceinline__ float4 codes4(uint32_t w, float s) {
+  const uint32_t u = w ^ 0x80808080u;
+  constexpr float kOff = 8388736.f;
+  return make_float4((__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)) - kOff) * s,
+                     (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441)) - kOff) * s,
+                     (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)) - kOff) * s,
+                     (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443)) - kOff) * s);
 }
-template <>
-__device__ __forceinline__ void put8<bf16>(bf16* p, const uint2 q, float s) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t src = i < 2 ? q.x : q.y;
-    const int b = (2 * i) & 3;
-    w[i] = (uint32_t)__bfloat16_as_ushort(f2bf(code_at(src, b) * s)) |
-           ((uint32_t)__bfloat16_as_ushort(f2bf(code_at(src, b + 1) * s)) << 16);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void put8(float* row, int lane, int half, const uint2 q, float s) {
+  reinterpret_cast<float4*>(row)[lane] = codes4(q.x, s);
+  reinterpret_cast<float4*>(row + half)[lane] = codes4(q.y, s);
+}
+__device__ __forceinline__ void put8(bf16* row, int lane, int, const uint2 q, float s) {
+  const float4 a = codes4(q.x, s), b = codes4(q.y, s);
+  const __nv_bfloat162 w[4] = {__floats2bfloat162_rn(a.x, a.y), __floats2bfloat162_rn(a.z, a.w),
+                               __floats2bfloat162_rn(b.x, b.y), __floats2bfloat162_rn(b.z, b.w)};
+  reinterpret_cast<uint4*>(row)[lane] = *reinterpret_cast<const uint4*>(w);
 }
 
 // The inverse of k_kv8_write: rows without a place read as zeros.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) k_kv8_read(const Kv8 c, const Kv8Rows r, const Kv8Io io, long long items) {
-  constexpr int LPR = D / 8;
+__global__ void __launch_bounds__(256) k_kv8_read(const Kv8 c, const Kv8Rows r, const Kv8Io io) {
+  constexpr int LPR = D / 8, RPB = 256 / LPR;
+  __shared__ PlaceSmem place;
   pdl_launch_dependents();
   pdl_wait();
-  const int sub = threadIdx.x % LPR;
-  const long long gstep = (long long)gridDim.x * (256 / LPR);
-  for (long long it = (long long)blockIdx.x * (256 / LPR) + threadIdx.x / LPR; it < items; it += gstep) {
-    const int tok = (int)(it / c.heads), head = (int)(it - (long long)tok * c.heads);
+  place_load(r, place);
+  const int sub = threadIdx.x % LPR, head = blockIdx.y;
+  T* kp = static_cast<T*>(io.k) + head * io.k_head;
+  T* vp = static_cast<T*>(io.v) + head * io.v_head;
+  __syncthreads();
+  for (long long t = (long long)blockIdx.x * RPB + threadIdx.x / LPR; t < r.n_rows; t += (long long)gridDim.x * RPB) {
     int slot = 0, pos = 0;
-    const bool ok = kv8_place(r, c.cap, tok, slot, pos);
-    uint2 qk = make_uint2(0, 0), qv = make_uint2(0, 0);
+    uint2 qk = make_uint2(0, 0), qv = qk;
     float sk = 0.f, sv = 0.f;
-    if (ok) {
+    if (kv8_place(r, place, c.cap, (int)t, slot, pos)) {
       const size_t row = ((size_t)slot * c.heads + head) * c.cap + pos;
-      qk = *reinterpret_cast<const uint2*>(c.k + row * D + sub * 8);
-      qv = *reinterpret_cast<const uint2*>(c.v + row * D + sub * 8);
+      qk = Vec8<T>::get_codes(c.k + row * D, sub, D / 2);
+      qv = Vec8<T>::get_codes(c.v + row * D, sub, D / 2);
       sk = c.k_scale[row];
       sv = c.v_scale[row];
     }
-    put8<T>(static_cast<T*>(io.k) + tok * io.k_tok + head * io.k_head + sub * 8, qk, sk);
-    put8<T>(static_cast<T*>(io.v) + tok * io.v_tok + head * io.v_head + sub * 8, qv, sv);
+    put8(kp + t * io.k_tok, sub, D / 2, qk, sk);
+    put8(vp + t * io.v_tok, sub, D / 2, qv, sv);
   }
 }
 
-int kv8_grid(long long items, int d, int unr) {
-  const long long per = 256 / (d / 8) * unr;
-  return (int)std::min<long long>((items + per - 1) / per, 148 * 8);
+// Blocks of 256 threads over tokens (x) and KV heads (y), up to 32 blocks per
+// SM (several waves: with 8 resident ones alone the ragged prefixes took 10 %
+// longer).
+dim3 kv8_grid(const Kv8& c, const Kv8Rows& r) {
+  const int per = 256 / (c.d / 8);
+  const int need = (r.n_rows - 1) / per + 1, most = std::max(1, 148 * 32 / c.heads);
+  return dim3(std::min(need, most), c.heads);
 }
 
 template <typename T, bool ROPE>
 cudaError_t kv8_write_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, const float2* cs, cudaStream_t st) {
-  const long long items = (long long)r.n_rows * c.heads;
-  const int grid = kv8_grid(items, c.d, 2);
   auto kern = c.d == 64 ? k_kv8_write<T, 64, ROPE> : c.d == 128 ? k_kv8_write<T, 128, ROPE> : k_kv8_write<T, 256, ROPE>;
-  return launch_ex(kern, dim3(grid), dim3(256), 0, st, 1, true, c, r, io, cs, items);
+  return launch_ex(kern, kv8_grid(c, r), dim3(256), 0, st, 1, true, c, r, io, cs);
 }
 
 template <typename T>
 cudaError_t kv8_read_sel(const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st) {
-  const long long items = (long long)r.n_rows * c.heads;
-  const int grid = kv8_grid(items, c.d, 1);
   auto kern = c.d == 64 ? k_kv8_read<T, 64> : c.d == 128 ? k_kv8_read<T, 128> : k_kv8_read<T, 256>;
-  return launch_ex(kern, dim3(grid), dim3(256), 0, st, 1, true, c, r, io, items);
+  return launch_ex(kern, kv8_grid(c, r), dim3(256), 0, st, 1, true, c, r, io);
 }
 
 }  // namespace

@@ -120,6 +120,7 @@ bool known(int dtype) { return dtype == PAE_FP32 || dtype == PAE_BF16; }
 
 pae_status check_cache(const char* fn, const pae_kv8* c) {
   if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return fail(PAE_ERR_ARG, "%s: the cache or one of its pointers is NULL", fn);
+  if (c->n_kv_heads > 65535) return fail(PAE_ERR_UNSUPPORTED, "%s: n_kv_heads must be at most 65535", fn);
   if (c->n_slots < 1 || c->n_kv_heads < 1 || c->capacity < 1 || c->capacity > kMaxCapacity)
     return fail(PAE_ERR_ARG, "%s: n_slots, n_kv_heads and capacity must be positive (capacity at most 2^30)", fn);
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
@@ -141,6 +142,7 @@ pae_status kv8_io(const char* fn, bool write, const pae_kv8* cache, void* k, voi
   pae_status st = check_cache(fn, cache);
   if (st != PAE_OK) return st;
   if (!known(dtype)) return fail(PAE_ERR_ARG, "%s: dtype must be PAE_FP32 or PAE_BF16", fn);
+  if (n_rows > kMaxCapacity) return fail(PAE_ERR_UNSUPPORTED, "%s: n_rows must be at most 2^30", fn);
   if (n_rows < 0 || n_seq < 0 || n_seq > cache->n_slots)
     return fail(PAE_ERR_ARG, "%s: n_rows must be >= 0 and n_seq in [0, n_slots]", fn);
   if (!cu && n_seq != 1) return fail(PAE_ERR_ARG, "%s: cu_rows may be NULL only for one sequence", fn);
