@@ -21,13 +21,14 @@ cudaError_t launch_quantize_rows(bool in_bf16, const void* x, long long ldx, int
 // ------------------------------------------------------------- int8 product
 // y[t][f] = (sum_k x[t][k] w[f][k]) sx[t] sw[f], int32 sums.
 struct I8GemmPlan {
+  int cg;       // CTAs per tile (2: pairs of cta_group::2; not with swap)
   int swap;     // 1: weight rows on the MMA's M side, tokens on its N side
   int tn;       // N tile (multiple of 16, 16..256)
   int tiles_m, tiles_n;
   int th;       // swap: weight rows per tile (32, 64 or 128; the MMA always spans 128)
   int splits;   // split-K cluster size (swap only)
   int stages;
-  int ctas;     // persistent grid (swap == 0)
+  int ctas;     // persistent grid (swap == 0), in tiles in flight
 };
 I8GemmPlan plan_i8_gemm(int tokens, int n, int k);
 struct I8GemmArgs {
@@ -36,12 +37,18 @@ struct I8GemmArgs {
   void* y;
   long long ldy;
   int tokens, n, k;
+  int tma_out;  // set by the launch
   int w_ready;  // 1: no kernel of the stream still writes the weights, so they may be read before the previous one ends
   DevErr err;
 };
 cudaError_t i8_gemm_init();
-cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols, const I8GemmPlan& p,
-                           const I8GemmArgs& a, cudaStream_t st);
+// tm_rows / tm_cols: the operands on the MMA's M and N side, boxes of 128 bytes
+// x i8_rows_box / i8_cols_box rows; tm_out (null: plain stores): the output,
+// boxes of 32 rows x 128 bytes.
+inline int i8_rows_box(const I8GemmPlan& p) { return p.swap ? p.th : 128; }
+inline int i8_cols_box(const I8GemmPlan& p) { return p.swap ? p.tn : p.tn / p.cg; }
+cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols,
+                           const CUtensorMap* tm_out, const I8GemmPlan& p, const I8GemmArgs& a, cudaStream_t st);
 
 // ---------------------------------------------------------------- K/V cache
 struct Kv8 {

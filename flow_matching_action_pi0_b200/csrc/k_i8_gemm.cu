@@ -10,7 +10,12 @@
 // of tokens:
 //   tokens on the rows   (many tokens) a persistent grid walks the tiles; the
 //                        accumulator is double-buffered in TMEM, so the
-//                        epilogue of a tile runs under the next one's MMAs
+//                        epilogue of a tile runs under the next one's MMAs.
+//                        Where filling shared memory bounds the loop (8-bit
+//                        MMAs eat 96 bytes per cycle of a 128 x 256 tile, an
+//                        SM gets about 64 from L2), two CTAs share a tile of
+//                        256 rows (cta_group::2): each brings 128 token rows
+//                        and half of the weight rows, 64 bytes per cycle
 //   weights on the rows  (few tokens: streaming the weights is what bounds
 //                        it) tokens pad only to a multiple of 16; tiles of 32
 //                        to 128 weight rows spread the weights over the SMs,
@@ -71,13 +76,14 @@ __host__ __device__ inline uint32_t tmem_cols(int n) {
   return c;
 }
 
-// Shared memory: ring | barriers | per-tile column scales / int32 partials.
+// Shared memory: ring | output boxes | barriers | per-tile column scales | int32 partials.
 struct I8Smem {
-  uint32_t bar_off, sw_off, part_off, total;
+  uint32_t out_off, bar_off, sw_off, part_off, total;
 };
 __host__ __device__ inline I8Smem i8_layout(const I8GemmPlan& p) {
   I8Smem L;
-  L.bar_off = stage_bytes(p.tn) * (uint32_t)p.stages;
+  L.out_off = stage_bytes(p.swap ? p.tn : p.tn / p.cg) * (uint32_t)p.stages;  // output boxes: 4 warps x 2 x 4 KB
+  L.bar_off = L.out_off + (p.swap ? 0u : 32768u);
   L.sw_off = L.bar_off + 512;
   L.part_off = L.sw_off + 2 * 256 * 4;
   L.total = L.part_off + (p.swap && p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u) + 1024;
@@ -119,10 +125,99 @@ __device__ __forceinline__ void store16(bf16* p, const float* v, int n, bool vec
 }
 
 // ------------------------------------------------------- tokens on the rows
-template <typename TO>
+// cta_group::2 forms: the MMA and its commit are issued by rank 0 of the pair;
+// the loads of both CTAs complete on rank 0's barrier.
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive on the barrier at this offset in both CTAs once the MMAs so far finish.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* tm, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Wait on an own barrier that the peer CTA arrives at.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, long long limit_ns) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((long long)(globaltimer_ns() - t0) > limit_ns) return false;
+  }
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_and_128(int id, bool v) {
+  __syncwarp();
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+// One lane of a converged warp (the loops below are walked by whole warps, so
+// that stage addresses and descriptors live in uniform registers).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Stage and phase of a ring position, stepped without divisions (the ring
+// length is a run-time number, and both threads of the pipeline take a step
+// every few hundred cycles).
+struct RingPos {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// CG CTAs per tile of 128 CG token rows x tn weight rows, neighbours along x (a
+// cluster of 2 for pairs).  tmY: the output, boxes of 32 rows x 128
+// bytes (only used with a.tma_out).
+template <typename TO, int CG>
 __global__ void __launch_bounds__(256, 1)
-    k_i8_gemm(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC, const I8GemmPlan p,
-              const I8GemmArgs a) {
+    k_i8_gemm(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC,
+              const __grid_constant__ CUtensorMap tmY, const I8GemmPlan p, const I8GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const I8Smem L = i8_layout(p);
@@ -130,14 +225,17 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* empty = full + p.stages;
   uint64_t* acc_full = empty + p.stages;  // [2]
   uint64_t* acc_empty = acc_full + 2;     // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sw = reinterpret_cast<float*>(smem + L.sw_off);  // [2][256]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const int rank = CG == 2 ? (int)(blockIdx.x & 1) : 0, first = blockIdx.x / CG, step = gridDim.x / CG;
   const int nkb = (a.k + KB - 1) / KB;
   const int tiles = p.tiles_m * p.tiles_n;
   const uint32_t ncols = tmem_cols(2 * p.tn);
-  const uint32_t sbytes = stage_bytes(p.tn);
+  const int brows = p.tn / CG;                                   // weight rows this CTA brings
+  const uint32_t sbytes = (uint32_t)(128 + brows) * KB;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -146,146 +244,241 @@ __global__ void __launch_bounds__(256, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 128);
+      mbar_init(&acc_empty[i], CG);
     }
+    mbar_init(drain, 1);
     s_flag[0] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmR);
     tma_prefetch_desc(&tmC);
+    if (a.tma_out) tma_prefetch_desc(&tmY);
   }
   if (warp == 2) {
-    tmem_alloc(tmem_slot, ncols);
-    tmem_relinquish();
+    if constexpr (CG == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(ncols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(tmem_slot, ncols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (CG == 2) cluster_sync();  // both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
   pdl_wait();  // the token codes and scales come from the quantiser
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
+    // ---------------------------------------------------------------- loads
+    RingPos r;
     int it = 0;
     bool good = true;
-    for (int tile = blockIdx.x; tile < tiles && good; tile += gridDim.x) {
+    for (int tile = first; tile < tiles && good; tile += step) {
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int st = it % p.stages;
-        if (it >= p.stages && !mbar_wait(&empty[st], ((it / p.stages) & 1) ^ 1, a.err.wait_ns)) {
+      const int y_r = (tm * CG + rank) * 128, y_c = tn * p.tn + rank * brows;
+      for (int kb = 0; kb < nkb; ++kb, ++it, r.next(p.stages)) {
+        good = __all_sync(0xffffffffu, it < p.stages || mbar_wait(&empty[r.st], r.ph ^ 1, a.err.wait_ns));
+        if (!good) {
           s_flag[0] = 1;
           set_error(a.err, DEV_TIMEOUT);
-          good = false;
           break;
         }
-        uint8_t* s = smem + (size_t)st * sbytes;
-        mbar_arrive_expect_tx(&full[st], sbytes);
-        tma_load_2d(s, &tmR, kb * KB, tm * 128, &full[st]);
-        tma_load_2d(s + 128 * KB, &tmC, kb * KB, tn * p.tn, &full[st]);
+        uint8_t* s = smem + (uint32_t)r.st * sbytes;
+        if (elect_one()) {
+          if constexpr (CG == 2) {
+            const uint32_t bar = map_cluster(smem_u32(&full[r.st]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(&full[r.st], 2 * sbytes);  // both CTAs' bytes
+            tma_load_2d_pair(s, &tmR, kb * KB, y_r, bar);
+            tma_load_2d_pair(s + 128 * KB, &tmC, kb * KB, y_c, bar);
+          } else {
+            mbar_arrive_expect_tx(&full[r.st], sbytes);
+            tma_load_2d(s, &tmR, kb * KB, y_r, &full[r.st]);
+            tma_load_2d(s + 128 * KB, &tmC, kb * KB, y_c, &full[r.st]);
+          }
+        }
+        __syncwarp();
       }
     }
-    // loads still in flight must land before this CTA may exit
-    for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
-      if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
-  } else if (warp == 1 && lane == 0) {
-    const uint32_t idesc = idesc_i8(128, p.tn);
-    int it = 0, n = 0;
+    // loads still in flight must land before this CTA may exit (the peer's land
+    // on rank 0's barriers, and no CTA leaves before rank 0 has seen them)
+    if (rank == 0 && lane == 0)
+      for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
+        if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
+  } else if (warp == 1 && rank == 0) {
+    // ----------------------------------------------------------------- MMA
+    const uint32_t idesc = idesc_i8(128 * CG, p.tn);
+    const uint64_t a0 = sw128_desc(smem_u32(smem), 16, 1024), b0 = sw128_desc(smem_u32(smem) + 128 * KB, 16, 1024);
+    RingPos r;
+    int n = 0;
     bool good = true;
-    for (int tile = blockIdx.x; tile < tiles && good; tile += gridDim.x, ++n) {
+    for (int tile = first; tile < tiles && good; tile += step, ++n) {
       const int buf = n & 1;
-      if (n >= 2 && !mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1, a.err.wait_ns)) good = false;
-      for (int kb = 0; kb < nkb && good; ++kb, ++it) {
-        const int st = it % p.stages;
-        if (!mbar_wait(&full[st], (it / p.stages) & 1, a.err.wait_ns)) {
-          good = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t sa = smem_u32(smem + (size_t)st * sbytes);
-        const uint64_t ad = sw128_desc(sa, 16, 1024), bd = sw128_desc(sa + 128 * KB, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < KB / 32; ++kk)
-          umma_i8(tmem + buf * p.tn, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, (kb | kk) != 0 ? 1u : 0u);
-        umma_commit(&empty[st]);
+      if (n >= 2) {
+        const uint32_t par = ((n >> 1) & 1) ^ 1;
+        good = CG == 2 ? mbar_wait_cluster(&acc_empty[buf], par, a.err.wait_ns) : mbar_wait(&acc_empty[buf], par, a.err.wait_ns);
+        good = __all_sync(0xffffffffu, good);
       }
-      if (good) umma_commit(&acc_full[buf]);
+      const uint32_t d = tmem + buf * p.tn;
+      for (int kb = 0; kb < nkb && good; ++kb, r.next(p.stages)) {
+        good = __all_sync(0xffffffffu, mbar_wait(&full[r.st], r.ph, a.err.wait_ns));
+        if (!good) break;
+        tc_fence_after();
+        const uint64_t ad = desc_add(a0, (uint32_t)r.st * sbytes), bd = desc_add(b0, (uint32_t)r.st * sbytes);
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < KB / 32; ++kk) {
+            const uint32_t acc = (kb | kk) != 0 ? 1u : 0u;
+            if constexpr (CG == 2)
+              umma_i8_pair(d, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, acc);
+            else
+              umma_i8(d, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, acc);
+          }
+          if constexpr (CG == 2) {
+            umma_commit_pair(&empty[r.st]);
+            if (kb == nkb - 1) umma_commit_pair(&acc_full[buf]);
+          } else {
+            umma_commit(&empty[r.st]);
+            if (kb == nkb - 1) umma_commit(&acc_full[buf]);
+          }
+        }
+        __syncwarp();
+      }
     }
     if (!good) {
       s_flag[0] = 1;
       set_error(a.err, DEV_TIMEOUT);
     }
-    // every MMA this thread issued must finish before TMEM is freed
-    uint64_t* drain = reinterpret_cast<uint64_t*>(smem + L.bar_off + 504);
-    mbar_init(drain, 1);
-    fence_mbar_init();
-    umma_commit(drain);
-    if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+    // every MMA issued must finish before TMEM is freed (the elected lane is the
+    // same one each time)
+    if (elect_one()) {
+      if constexpr (CG == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(drain)) : "memory");
+      else
+        umma_commit(drain);
+      if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+    }
   } else if (warp >= 4) {
-    const int et = threadIdx.x - 128;  // row of the tile = TMEM lane
+    // ------------------------------------------------------------ epilogue
+    // Thread = row.  Columns go through the warp's two 4 KB buffers (32 rows of
+    // 128 bytes, swizzled) and leave as bulk tensor stores, which clip at the
+    // matrix's edges; outputs that a tensor map cannot describe are stored from
+    // the registers.
+    constexpr int CPB = 128 / (int)sizeof(TO);  // columns per 128-byte box
+    const int et = threadIdx.x - 128;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t stage = smem_u32(smem + L.out_off) + (uint32_t)(warp & 3) * 8192u;
     TO* y = static_cast<TO*>(a.y);
     const bool vec = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && (a.ldy * (long long)sizeof(TO)) % 16 == 0;
-    int n = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
+    int n = 0, stores = 0;
+    for (int tile = first; tile < tiles; tile += step, ++n) {
       const int buf = n & 1;
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
-      const int t = tm * 128 + et, f0 = tn * p.tn;
+      const int row0 = (tm * CG + rank) * 128, t = row0 + et, f0 = tn * p.tn;
       float* sw = s_sw + buf * 256;
-      for (int i = et; i < p.tn; i += 128) sw[i] = f0 + i < a.n ? a.sw[f0 + i] : 0.f;
+      for (int i = et; i < p.tn; i += 128) sw[i] = f0 + i < a.n ? __ldg(a.sw + f0 + i) : 0.f;
       const float sx = t < a.tokens ? a.sx[t] : 0.f;
       // the column scales are in place for all four warps, and all go on or stop
       const bool got = mbar_wait(&acc_full[buf], (n >> 1) & 1, a.err.wait_ns);
-      __syncwarp();
-      uint32_t go;
-      asm volatile(
-          "{\n\t.reg .pred p, q;\n\t"
-          "setp.ne.u32 p, %1, 0;\n\t"
-          "bar.red.and.pred q, 1, 128, p;\n\t"
-          "selp.u32 %0, 1, 0, q;\n\t}"
-          : "=r"(go)
-          : "r"((uint32_t)(got && s_flag[0] == 0))
-          : "memory");
-      if (!go) {
+      if (!bar_and_128(1, got && s_flag[0] == 0)) {
         set_error(a.err, DEV_TIMEOUT);
         break;
       }
       tc_fence_after();
+      const uint32_t acc0 = tmem + buf * p.tn + lane_off;
       int acc[2][16];
-      tmem_ld16i(tmem + buf * p.tn + lane_off, acc[0]);
+      tmem_ld16i(acc0, acc[0]);
       const int nc = p.tn / 16;
-      auto emit = [&](int c, int* v) {
-        if (t < a.tokens && f0 + c * 16 < a.n) {
-          float o[16];
+      auto emit = [&](int c, const int* v) {
+        float o[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
-            o[4 * q] = (float)v[4 * q] * sx * w.x;
-            o[4 * q + 1] = (float)v[4 * q + 1] * sx * w.y;
-            o[4 * q + 2] = (float)v[4 * q + 2] * sx * w.z;
-            o[4 * q + 3] = (float)v[4 * q + 3] * sx * w.w;
+        for (int q = 0; q < 4; ++q) {
+          const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
+          o[4 * q] = (float)v[4 * q] * sx * w.x;
+          o[4 * q + 1] = (float)v[4 * q + 1] * sx * w.y;
+          o[4 * q + 2] = (float)v[4 * q + 2] * sx * w.z;
+          o[4 * q + 3] = (float)v[4 * q + 3] * sx * w.w;
+        }
+        if (!a.tma_out) {
+          if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
+          return;
+        }
+        const int in_box = c % (CPB / 16);  // 16 columns: 2 (bf16) or 4 (fp32) chunks of a box's 8
+        const uint32_t box = stage + (uint32_t)(stores & 1) * 4096u;
+        if (in_box == 0) {
+          // the store that last read this buffer is done reading
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+        }
+        const uint32_t rowp = box + (uint32_t)lane * 128u;
+        if constexpr (sizeof(TO) == 2) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * i], o[8 * q + 2 * i + 1]);
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + (uint32_t)(((in_box * 2 + q) ^ (lane & 7)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
-          store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + (uint32_t)(((in_box * 4 + q) ^ (lane & 7)) << 4)),
+                         "r"(__float_as_uint(o[4 * q])), "r"(__float_as_uint(o[4 * q + 1])),
+                         "r"(__float_as_uint(o[4 * q + 2])), "r"(__float_as_uint(o[4 * q + 3]))
+                         : "memory");
+        }
+        if (in_box == CPB / 16 - 1) {  // the box is full
+          fence_proxy_async_smem();
+          __syncwarp();
+          const int x = f0 + (c - in_box) * 16, yr = row0 + (warp & 3) * 32;
+          if (lane == 0) {
+            if (x < a.n && yr < a.tokens) tma_store_2d(&tmY, box, x, yr);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          ++stores;
         }
       };
       for (int c = 0; c < nc; c += 2) {
         tmem_ld_wait();
         reg_fence16i(acc[0]);
-        if (c + 1 < nc) tmem_ld16i(tmem + buf * p.tn + lane_off + (c + 1) * 16, acc[1]);
+        if (c + 1 < nc) tmem_ld16i(acc0 + (c + 1) * 16, acc[1]);
         emit(c, acc[0]);
         if (c + 1 < nc) {
           tmem_ld_wait();
           reg_fence16i(acc[1]);
-          if (c + 2 < nc) tmem_ld16i(tmem + buf * p.tn + lane_off + (c + 2) * 16, acc[0]);
+          if (c + 2 < nc) tmem_ld16i(acc0 + (c + 2) * 16, acc[0]);
           emit(c + 1, acc[1]);
         }
       }
+      // this CTA's four warps are done with the accumulator
       tc_fence_before();
-      mbar_arrive(&acc_empty[buf]);
+      bar_and_128(2, true);
+      if (et == 0) {
+        if constexpr (CG == 2)
+          mbar_arrive_cluster(map_cluster(smem_u32(&acc_empty[buf]), 0));
+        else
+          mbar_arrive(&acc_empty[buf]);
+      }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // every store has left shared memory
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) tmem_dealloc(tmem, ncols);
+  if constexpr (CG == 2) cluster_sync();  // no CTA frees or leaves what the pair still uses
+  if (warp == 2) {
+    if constexpr (CG == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(ncols) : "memory");
+    else
+      tmem_dealloc(tmem, ncols);
+  }
 }
 
 // ------------------------------------------------------ weights on the rows
@@ -461,13 +654,13 @@ __global__ void __launch_bounds__(256, 1)
 
 // Tokens go to the N side while they fit one tile of at most 64: the weights
 // are then read once and padding stays under 16 tokens.  With more, tokens on
-// the rows; the N tile is the one whose waves of 148 CTAs cost least, a tile's
-// cost being its operand bytes (shared-memory fills bound the main loop) plus
-// a fixed start and end.
+// the rows; one or two CTAs per tile and the N tile are those whose waves over
+// the 148 SMs cost least.
 I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
   I8GemmPlan p{};
   const int nkb = (k + KB - 1) / KB;
   p.splits = 1;
+  p.cg = 1;
   if (tokens <= 64) {
     p.swap = 1;
     p.tn = std::max(16, (tokens + 15) / 16 * 16);
@@ -480,21 +673,27 @@ I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
     const uint32_t part = p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u;
     p.stages = std::min({8, (nkb + p.splits - 1) / p.splits, (int)((196u * 1024u - part) / stage_bytes(p.tn))});
   } else {
-    p.tiles_m = (tokens + 127) / 128;
+    // cycles of one k block: the fill at 64 bytes per cycle, or the four MMAs (a
+    // narrow one still reads its 128 rows); 3000 for a tile's start and end
     double best = 0;
-    for (int tn = 32; tn <= 256; tn += 16) {
-      if (tn > 32 && tn - 16 >= n) break;
-      const int tiles = p.tiles_m * ((n + tn - 1) / tn);
-      const int waves = (tiles + 147) / 148;
-      const double cost = waves * ((double)nkb * (128 + tn) + 1200.0);
-      if (p.tn == 0 || cost < best * 0.999) {
-        best = cost;
-        p.tn = tn;
+    for (int cg = 1; cg <= 2; ++cg) {
+      const int tm = (tokens + 128 * cg - 1) / (128 * cg), units = 148 / cg;
+      for (int tn = 32; tn <= 256; tn += 16 * cg) {
+        if (tn > 32 && tn - 16 * cg >= n) break;
+        const long long tiles = (long long)tm * ((n + tn - 1) / tn);
+        const double fill = 2.0 * (128 + tn / cg), mma = 4.0 * std::max(tn / 2, 32 + tn / 4 / cg);
+        const double cost = (double)((tiles + units - 1) / units) * nkb * std::max(fill, mma) + 3000.0;
+        if (p.tn == 0 || cost < best * 0.999) {
+          best = cost;
+          p.tn = tn;
+          p.cg = cg;
+          p.tiles_m = tm;
+        }
       }
     }
     p.tiles_n = (n + p.tn - 1) / p.tn;
-    p.ctas = std::min(148, p.tiles_m * p.tiles_n);
-    p.stages = std::min(8, (int)(196u * 1024u / stage_bytes(p.tn)));
+    p.ctas = std::min(148 / p.cg, p.tiles_m * p.tiles_n);
+    p.stages = std::min(8, (int)(160u * 1024u / stage_bytes(p.tn / p.cg)));
   }
   p.stages = std::max(2, p.stages);
   return p;
@@ -506,26 +705,45 @@ cudaError_t i8_gemm_init() {
   auto set = [&](auto kern) {
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   };
-  set(k_i8_gemm<float>);
-  set(k_i8_gemm<bf16>);
+  set(k_i8_gemm<float, 1>);
+  set(k_i8_gemm<bf16, 1>);
+  set(k_i8_gemm<float, 2>);
+  set(k_i8_gemm<bf16, 2>);
   set(k_i8_gemm_few<float>);
   set(k_i8_gemm_few<bf16>);
   return e;
 }
 
 template <typename TO>
-static cudaError_t i8_launch(const CUtensorMap& r, const CUtensorMap& c, const I8GemmPlan& p, const I8GemmArgs& a,
-                             cudaStream_t st) {
+static cudaError_t i8_launch(const CUtensorMap& r, const CUtensorMap& c, const CUtensorMap& y, const I8GemmPlan& p,
+                             const I8GemmArgs& a, cudaStream_t st) {
   const size_t smem = i8_layout(p).total;
   if (p.swap)
     return launch_ex(k_i8_gemm_few<TO>, dim3(p.tiles_m, p.splits, p.tiles_n), dim3(256), smem, st, p.splits, true, r,
                      c, p, a);
-  return launch_ex(k_i8_gemm<TO>, dim3(p.ctas), dim3(256), smem, st, 1, true, r, c, p, a);
+  if (p.cg == 1) return launch_ex(k_i8_gemm<TO, 1>, dim3(p.ctas), dim3(256), smem, st, 1, true, r, c, y, p, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.ctas);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeClusterDimension;  // pairs lie along x
+  at[0].val.clusterDim.x = 2;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_i8_gemm<TO, 2>, r, c, y, p, a);
 }
 
-cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols, const I8GemmPlan& p,
-                           const I8GemmArgs& a, cudaStream_t st) {
-  return out_bf16 ? i8_launch<bf16>(*tm_rows, *tm_cols, p, a, st) : i8_launch<float>(*tm_rows, *tm_cols, p, a, st);
+cudaError_t launch_i8_gemm(bool out_bf16, const CUtensorMap* tm_rows, const CUtensorMap* tm_cols,
+                           const CUtensorMap* tm_out, const I8GemmPlan& p, const I8GemmArgs& a, cudaStream_t st) {
+  I8GemmArgs b = a;
+  b.tma_out = tm_out != nullptr;
+  const CUtensorMap& y = tm_out ? *tm_out : *tm_rows;  // (not read without tma_out)
+  return out_bf16 ? i8_launch<bf16>(*tm_rows, *tm_cols, y, p, b, st) : i8_launch<float>(*tm_rows, *tm_cols, y, p, b, st);
 }
 
 }  // namespace pae

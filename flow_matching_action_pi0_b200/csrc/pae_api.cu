@@ -1641,15 +1641,15 @@ static pae_status produce_prefix_w8a8(pae_ctx* ctx, int row, const void* const* 
   const int kvr = 2 * s.Hkv * s.d;
   const I8GemmPlan p = plan_i8_gemm(len, kvr, s.Dp);
   CUtensorMap tx, tw;
-  pae_status st = make_map_i8(ctx, &tx, ctx->x8, s.Dp, len, p.swap ? p.tn : 128);
+  pae_status st = make_map_i8(ctx, &tx, ctx->x8, s.Dp, len, p.swap ? i8_cols_box(p) : i8_rows_box(p));
   if (st != PAE_OK) return st;
-  const I8GemmArgs base{ctx->x8_scale, nullptr, ctx->y8, kvr, len, kvr, s.Dp, 1, DevErr{ctx->err_dev, ctx->wait_ns}};
+  const I8GemmArgs base{ctx->x8_scale, nullptr, ctx->y8, kvr, len, kvr, s.Dp, 0, 1, DevErr{ctx->err_dev, ctx->wait_ns}};
   for (int l = 0; l < s.L; ++l) {
-    if ((st = make_map_i8(ctx, &tw, ctx->w8 + (size_t)l * kvr * s.Dp, s.Dp, kvr, p.swap ? p.th : p.tn)) != PAE_OK) return st;
+    if ((st = make_map_i8(ctx, &tw, ctx->w8 + (size_t)l * kvr * s.Dp, s.Dp, kvr, p.swap ? i8_rows_box(p) : i8_cols_box(p))) != PAE_OK) return st;
     CK(launch_quantize_rows(true, h_per_layer[l], s.Dp, len, s.Dp, s.eps, ctx->x8, ctx->x8_scale, stm));
     I8GemmArgs a = base;
     a.sw = ctx->w8_scale + (size_t)l * kvr;
-    CK(launch_i8_gemm(false, p.swap ? &tw : &tx, p.swap ? &tx : &tw, p, a, stm));
+    CK(launch_i8_gemm(false, p.swap ? &tw : &tx, p.swap ? &tx : &tw, nullptr, p, a, stm));
     CK(launch_kv8_write(false, layer_cache8(ctx, l), Kv8Rows{nullptr, nullptr, 1, len, row},
                         Kv8Io{ctx->y8, ctx->y8 + s.Hkv * s.d, kvr, s.d, kvr, s.d}, ctx->rope_cs, stm));
   }

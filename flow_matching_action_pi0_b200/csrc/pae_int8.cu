@@ -249,16 +249,25 @@ pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signe
   pae_status st = device_state(fn, stream, true, &d);
   if (st != PAE_OK) return st;
   const I8GemmPlan p = plan_i8_gemm(tokens, n, k);
-  CUtensorMap rows, cols;
-  if (p.swap) {
-    if ((st = make_map(d, &rows, w, n, k, p.th)) != PAE_OK) return st;
-    if ((st = make_map(d, &cols, x, tokens, k, p.tn)) != PAE_OK) return st;
-  } else {
-    if ((st = make_map(d, &rows, x, tokens, k, 128)) != PAE_OK) return st;
-    if ((st = make_map(d, &cols, w, n, k, p.tn)) != PAE_OK) return st;
+  CUtensorMap rows, cols, out;
+  if ((st = make_map(d, &rows, p.swap ? w : x, p.swap ? n : tokens, k, i8_rows_box(p))) != PAE_OK) return st;
+  if ((st = make_map(d, &cols, p.swap ? x : w, p.swap ? tokens : n, k, i8_cols_box(p))) != PAE_OK) return st;
+  const size_t es = dtype == PAE_BF16 ? 2 : 4;
+  // whole boxes of 128 bytes per tile: a box may not reach into the next tile's columns
+  const bool tma = !p.swap && p.tn % (128 / es) == 0 && aligned(y, 16) && (size_t)ldy * es % 16 == 0 && (size_t)ldy * es < (1ULL << 40);
+  if (tma) {
+    cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)tokens};
+    cuuint64_t strides[1] = {(cuuint64_t)ldy * es};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / es), 32};
+    cuuint32_t el[2] = {1, 1};
+    const CUresult r = d->encode(&out, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, y, dims,
+                                 strides, box, el, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(PAE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for the output", (int)r);
   }
-  const I8GemmArgs a{x_scale, w_scale, y, ldy, tokens, n, k, 0, DevErr{d->err_dev, kWaitNs}};
-  const cudaError_t e = launch_i8_gemm(dtype == PAE_BF16, &rows, &cols, p, a, reinterpret_cast<cudaStream_t>(stream));
+  const I8GemmArgs a{x_scale, w_scale, y, ldy, tokens, n, k, 0, 0, DevErr{d->err_dev, kWaitNs}};
+  const cudaError_t e = launch_i8_gemm(dtype == PAE_BF16, &rows, &cols, tma ? &out : nullptr, p, a,
+                                       reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PAE_OK : cuda_fail(fn, e);
 }
 
