@@ -30,7 +30,7 @@ struct I8GemmPlan {
   int stages;
   int ctas;     // persistent grid (swap == 0), in tiles in flight
 };
-I8GemmPlan plan_i8_gemm(int tokens, int n, int k);
+I8GemmPlan plan_i8_gemm(int tokens, int n, int k, int out_bytes /* of an output element */);
 struct I8GemmArgs {
   const float* sx;
   const float* sw;

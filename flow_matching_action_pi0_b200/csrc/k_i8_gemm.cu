@@ -24,8 +24,8 @@
 //                        SMs stream weights, and the int32 partials are summed
 //                        through distributed shared memory
 // Warp 0 streams both operands by TMA in 128-byte k blocks (128-byte swizzle)
-// through a ring of stages, warp 1 issues the MMAs (K = 32 codes each), warps
-// 4-7 read the accumulator (thread = TMEM lane = row).
+// through a ring of stages, warp 1 issues the MMAs (K = 32 codes each), the
+// warps from 4 on read the accumulator (thread = TMEM lane = row).
 #include <algorithm>
 
 #include "int8.h"
@@ -82,7 +82,7 @@ struct I8Smem {
 };
 __host__ __device__ inline I8Smem i8_layout(const I8GemmPlan& p) {
   I8Smem L;
-  L.out_off = stage_bytes(p.swap ? p.tn : p.tn / p.cg) * (uint32_t)p.stages;  // output boxes: 4 warps x 2 x 4 KB
+  L.out_off = stage_bytes(p.swap ? p.tn : p.tn / p.cg) * (uint32_t)p.stages;  // output boxes: 8 warps x 4 KB
   L.bar_off = L.out_off + (p.swap ? 0u : 32768u);
   L.sw_off = L.bar_off + 512;
   L.part_off = L.sw_off + 2 * 256 * 4;
@@ -170,19 +170,24 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if ((long long)(globaltimer_ns() - t0) > limit_ns) return false;
   }
 }
+__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(tm)),
                "r"(src), "r"(x), "r"(y)
                : "memory");
 }
-__device__ __forceinline__ bool bar_and_128(int id, bool v) {
+constexpr int kEpiWarps = 8;  // epilogue warps: two per TMEM lane quarter, taking turns by box of columns
+constexpr int kThreads = 128 + kEpiWarps * 32;
+__device__ __forceinline__ bool bar_and_epi(int id, bool v) {
   __syncwarp();
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, %2, 128, p;\n\t"
+      "bar.red.and.pred q, %2, 256, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
       : "r"((uint32_t)v), "r"(id)
@@ -215,7 +220,7 @@ struct RingPos {
 // cluster of 2 for pairs).  tmY: the output, boxes of 32 rows x 128
 // bytes (only used with a.tma_out).
 template <typename TO, int CG>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_i8_gemm(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC,
               const __grid_constant__ CUtensorMap tmY, const I8GemmPlan p, const I8GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -362,104 +367,96 @@ __global__ void __launch_bounds__(256, 1)
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ epilogue
-    // Thread = row.  Columns go through the warp's two 4 KB buffers (32 rows of
-    // 128 bytes, swizzled) and leave as bulk tensor stores, which clip at the
-    // matrix's edges; outputs that a tensor map cannot describe are stored from
-    // the registers.
-    constexpr int CPB = 128 / (int)sizeof(TO);  // columns per 128-byte box
-    const int et = threadIdx.x - 128;
+    // Thread = row; the two warps of a lane quarter take the 128-byte boxes of
+    // columns in turn.  A box goes through the warp's 4 KB buffer (32 rows,
+    // swizzled) and leaves as one bulk tensor store, which clips at the matrix's
+    // edges; outputs that a tensor map cannot describe are stored from the
+    // registers.
+    constexpr int CPB = 128 / (int)sizeof(TO), NB = CPB / 16;  // columns and 16-column chunks per box
+    const int et = threadIdx.x - 128, half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t stage = smem_u32(smem + L.out_off) + (uint32_t)(warp & 3) * 8192u;
+    const uint32_t box = smem_u32(smem + L.out_off) + (uint32_t)(warp - 4) * 4096u;
     TO* y = static_cast<TO*>(a.y);
     const bool vec = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && (a.ldy * (long long)sizeof(TO)) % 16 == 0;
-    int n = 0, stores = 0;
+    const int nc = p.tn / 16;
+    int n = 0;
     for (int tile = first; tile < tiles; tile += step, ++n) {
       const int buf = n & 1;
       const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
-      const int row0 = (tm * CG + rank) * 128, t = row0 + et, f0 = tn * p.tn;
+      const int row0 = (tm * CG + rank) * 128, t = row0 + row, f0 = tn * p.tn;
       float* sw = s_sw + buf * 256;
-      for (int i = et; i < p.tn; i += 128) sw[i] = f0 + i < a.n ? __ldg(a.sw + f0 + i) : 0.f;
+      for (int i = et; i < p.tn; i += kEpiWarps * 32) sw[i] = f0 + i < a.n ? __ldg(a.sw + f0 + i) : 0.f;
       const float sx = t < a.tokens ? a.sx[t] : 0.f;
-      // the column scales are in place for all four warps, and all go on or stop
+      // the column scales are in place for all warps, and all go on or stop
       const bool got = mbar_wait(&acc_full[buf], (n >> 1) & 1, a.err.wait_ns);
-      if (!bar_and_128(1, got && s_flag[0] == 0)) {
+      if (!bar_and_epi(1, got && s_flag[0] == 0)) {
         set_error(a.err, DEV_TIMEOUT);
         break;
       }
       tc_fence_after();
       const uint32_t acc0 = tmem + buf * p.tn + lane_off;
-      int acc[2][16];
-      tmem_ld16i(acc0, acc[0]);
-      const int nc = p.tn / 16;
-      auto emit = [&](int c, const int* v) {
-        float o[16];
+      for (int b0 = half * NB; b0 < nc; b0 += 2 * NB) {  // this warp's boxes
+        int acc[NB][16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
-          o[4 * q] = (float)v[4 * q] * sx * w.x;
-          o[4 * q + 1] = (float)v[4 * q + 1] * sx * w.y;
-          o[4 * q + 2] = (float)v[4 * q + 2] * sx * w.z;
-          o[4 * q + 3] = (float)v[4 * q + 3] * sx * w.w;
+        for (int i = 0; i < NB; ++i)
+          if (b0 + i < nc) tmem_ld16i(acc0 + (b0 + i) * 16, acc[i]);
+        if (a.tma_out) {
+          // the store that last read the buffer is done reading
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         }
-        if (!a.tma_out) {
-          if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
-          return;
-        }
-        const int in_box = c % (CPB / 16);  // 16 columns: 2 (bf16) or 4 (fp32) chunks of a box's 8
-        const uint32_t box = stage + (uint32_t)(stores & 1) * 4096u;
-        if (in_box == 0) {
-          // the store that last read this buffer is done reading
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-          __syncwarp();
-        }
-        const uint32_t rowp = box + (uint32_t)lane * 128u;
-        if constexpr (sizeof(TO) == 2) {
+        __syncwarp();
+        tmem_ld_wait();
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            uint32_t w[4];
+        for (int i = 0; i < NB; ++i) reg_fence16i(acc[i]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * i], o[8 * q + 2 * i + 1]);
-              w[i] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + (uint32_t)(((in_box * 2 + q) ^ (lane & 7)) << 4)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
+        for (int i = 0; i < NB; ++i) {
+          const int c = b0 + i;
+          if (c >= nc) break;
+          float o[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
+            o[4 * q] = (float)acc[i][4 * q] * (sx * w.x);
+            o[4 * q + 1] = (float)acc[i][4 * q + 1] * (sx * w.y);
+            o[4 * q + 2] = (float)acc[i][4 * q + 2] * (sx * w.z);
+            o[4 * q + 3] = (float)acc[i][4 * q + 3] * (sx * w.w);
           }
-        } else {
+          if (!a.tma_out) {
+            if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
+            continue;
+          }
+          const uint32_t rowp = box + (uint32_t)lane * 128u;
+          if constexpr (sizeof(TO) == 2) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(rowp + (uint32_t)(((in_box * 4 + q) ^ (lane & 7)) << 4)),
-                         "r"(__float_as_uint(o[4 * q])), "r"(__float_as_uint(o[4 * q + 1])),
-                         "r"(__float_as_uint(o[4 * q + 2])), "r"(__float_as_uint(o[4 * q + 3]))
-                         : "memory");
+            for (int q = 0; q < 2; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * k], o[8 * q + 2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              sts128(rowp + (uint32_t)(((i * 2 + q) ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sts128(rowp + (uint32_t)(((i * 4 + q) ^ (lane & 7)) << 4), __float_as_uint(o[4 * q]),
+                     __float_as_uint(o[4 * q + 1]), __float_as_uint(o[4 * q + 2]), __float_as_uint(o[4 * q + 3]));
+          }
         }
-        if (in_box == CPB / 16 - 1) {  // the box is full
+        if (a.tma_out) {  // (tn is then a whole number of boxes)
           fence_proxy_async_smem();
           __syncwarp();
-          const int x = f0 + (c - in_box) * 16, yr = row0 + (warp & 3) * 32;
           if (lane == 0) {
+            const int x = f0 + b0 * 16, yr = row0 + (warp & 3) * 32;
             if (x < a.n && yr < a.tokens) tma_store_2d(&tmY, box, x, yr);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
-          ++stores;
-        }
-      };
-      for (int c = 0; c < nc; c += 2) {
-        tmem_ld_wait();
-        reg_fence16i(acc[0]);
-        if (c + 1 < nc) tmem_ld16i(acc0 + (c + 1) * 16, acc[1]);
-        emit(c, acc[0]);
-        if (c + 1 < nc) {
-          tmem_ld_wait();
-          reg_fence16i(acc[1]);
-          if (c + 2 < nc) tmem_ld16i(acc0 + (c + 2) * 16, acc[0]);
-          emit(c + 1, acc[1]);
         }
       }
-      // this CTA's four warps are done with the accumulator
+      // this CTA's epilogue warps are done with the accumulator
       tc_fence_before();
-      bar_and_128(2, true);
+      bar_and_epi(2, true);
       if (et == 0) {
         if constexpr (CG == 2)
           mbar_arrive_cluster(map_cluster(smem_u32(&acc_empty[buf]), 0));
@@ -656,7 +653,7 @@ __global__ void __launch_bounds__(256, 1)
 // are then read once and padding stays under 16 tokens.  With more, tokens on
 // the rows; one or two CTAs per tile and the N tile are those whose waves over
 // the 148 SMs cost least.
-I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
+I8GemmPlan plan_i8_gemm(int tokens, int n, int k, int out_bytes) {
   I8GemmPlan p{};
   const int nkb = (k + KB - 1) / KB;
   p.splits = 1;
@@ -673,16 +670,19 @@ I8GemmPlan plan_i8_gemm(int tokens, int n, int k) {
     const uint32_t part = p.splits > 1 ? 128u * (uint32_t)p.tn * 4u : 0u;
     p.stages = std::min({8, (nkb + p.splits - 1) / p.splits, (int)((196u * 1024u - part) / stage_bytes(p.tn))});
   } else {
-    // cycles of one k block: the fill at 64 bytes per cycle, or the four MMAs (a
-    // narrow one still reads its 128 rows); 3000 for a tile's start and end
+    // Measured cycles (fit over tiles of 32 to 256 columns at 300 to 7743 tokens):
+    // a k block costs its fill at about 60 bytes per cycle, or, for pairs, its
+    // MMAs; a tile 1100 more; pairs 2000 once.  Tiles are whole 128-byte boxes of
+    // the output wide (or 32), so that it can leave as bulk tensor stores.
+    const int box = 128 / out_bytes;
     double best = 0;
     for (int cg = 1; cg <= 2; ++cg) {
       const int tm = (tokens + 128 * cg - 1) / (128 * cg), units = 148 / cg;
-      for (int tn = 32; tn <= 256; tn += 16 * cg) {
-        if (tn > 32 && tn - 16 * cg >= n) break;
+      for (int tn = 32; tn <= 256; tn += tn < box ? box - tn : box) {
+        if (tn > 32 && tn - 32 >= n) break;
         const long long tiles = (long long)tm * ((n + tn - 1) / tn);
-        const double fill = 2.0 * (128 + tn / cg), mma = 4.0 * std::max(tn / 2, 32 + tn / 4 / cg);
-        const double cost = (double)((tiles + units - 1) / units) * nkb * std::max(fill, mma) + 3000.0;
+        const double kblock = cg == 1 ? 2.1 * (128 + tn) : std::max(2.2 * (128 + tn / 2), 2.85 * tn);
+        const double cost = (double)((tiles + units - 1) / units) * (nkb * kblock + 1100.0) + (cg == 2 ? 2000.0 : 0.0);
         if (p.tn == 0 || cost < best * 0.999) {
           best = cost;
           p.tn = tn;
@@ -721,10 +721,10 @@ static cudaError_t i8_launch(const CUtensorMap& r, const CUtensorMap& c, const C
   if (p.swap)
     return launch_ex(k_i8_gemm_few<TO>, dim3(p.tiles_m, p.splits, p.tiles_n), dim3(256), smem, st, p.splits, true, r,
                      c, p, a);
-  if (p.cg == 1) return launch_ex(k_i8_gemm<TO, 1>, dim3(p.ctas), dim3(256), smem, st, 1, true, r, c, y, p, a);
+  if (p.cg == 1) return launch_ex(k_i8_gemm<TO, 1>, dim3(p.ctas), dim3(kThreads), smem, st, 1, true, r, c, y, p, a);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.ctas);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[2];

@@ -1639,7 +1639,7 @@ pae_status pae_set_prefix(pae_ctx* ctx, int row, const void* const* k_per_layer,
 static pae_status produce_prefix_w8a8(pae_ctx* ctx, int row, const void* const* h_per_layer, int len, cudaStream_t stm) {
   const Shape& s = ctx->s;
   const int kvr = 2 * s.Hkv * s.d;
-  const I8GemmPlan p = plan_i8_gemm(len, kvr, s.Dp);
+  const I8GemmPlan p = plan_i8_gemm(len, kvr, s.Dp, 4);
   CUtensorMap tx, tw;
   pae_status st = make_map_i8(ctx, &tx, ctx->x8, s.Dp, len, p.swap ? i8_cols_box(p) : i8_rows_box(p));
   if (st != PAE_OK) return st;

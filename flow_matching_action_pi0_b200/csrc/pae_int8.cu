@@ -248,7 +248,7 @@ pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signe
   DeviceState* d = nullptr;
   pae_status st = device_state(fn, stream, true, &d);
   if (st != PAE_OK) return st;
-  const I8GemmPlan p = plan_i8_gemm(tokens, n, k);
+  const I8GemmPlan p = plan_i8_gemm(tokens, n, k, dtype == PAE_BF16 ? 2 : 4);
   CUtensorMap rows, cols, out;
   if ((st = make_map(d, &rows, p.swap ? w : x, p.swap ? n : tokens, k, i8_rows_box(p))) != PAE_OK) return st;
   if ((st = make_map(d, &cols, p.swap ? x : w, p.swap ? tokens : n, k, i8_cols_box(p))) != PAE_OK) return st;
