@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(256, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sx = reinterpret_cast<float*>(smem + L.sw_off);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int f0 = blockIdx.x * p.th, split = blockIdx.y, t0 = blockIdx.z * p.tn;
   const int nkb_all = (a.k + KB - 1) / KB;
   const int kb0 = (int)((long long)nkb_all * split / p.splits), kb1 = (int)((long long)nkb_all * (split + 1) / p.splits);
@@ -521,52 +521,63 @@ __global__ void __launch_bounds__(256, 1)
   const uint32_t tmem = *tmem_slot;
   pdl_launch_dependents();
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // Tiles of th < 128 weight rows fill the front of the A tile; the MMA's
     // remaining rows multiply whatever lies behind and are never read.
     const uint32_t tx = (uint32_t)(p.th + p.tn) * KB;
     if (!a.w_ready) pdl_wait();
     const int npre = min(nkb, p.stages);
-    for (int i = 0; i < npre; ++i) {
-      mbar_arrive_expect_tx(&full[i], tx);
-      tma_load_2d(smem + (size_t)i * sbytes, &tmW, (kb0 + i) * KB, f0, &full[i]);
-    }
-    pdl_wait();
-    for (int i = 0; i < npre; ++i)
-      tma_load_2d(smem + (size_t)i * sbytes + 128 * KB, &tmX, (kb0 + i) * KB, t0, &full[i]);
-    int it = npre;
-    for (; it < nkb; ++it) {
-      const int st = it % p.stages;
-      if (!mbar_wait(&empty[st], ((it / p.stages) & 1) ^ 1, a.err.wait_ns)) {
-        s_flag[0] = 1;
-        set_error(a.err, DEV_TIMEOUT);
-        break;
+    if (elect_one())
+      for (int i = 0; i < npre; ++i) {
+        mbar_arrive_expect_tx(&full[i], tx);
+        tma_load_2d(smem + (uint32_t)i * sbytes, &tmW, (kb0 + i) * KB, f0, &full[i]);
       }
-      uint8_t* s = smem + (size_t)st * sbytes;
-      mbar_arrive_expect_tx(&full[st], tx);
-      tma_load_2d(s, &tmW, (kb0 + it) * KB, f0, &full[st]);
-      tma_load_2d(s + 128 * KB, &tmX, (kb0 + it) * KB, t0, &full[st]);
-    }
-    for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
-      if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
-  } else if (warp == 1 && lane == 0) {
+    __syncwarp();
+    pdl_wait();
+    if (elect_one())
+      for (int i = 0; i < npre; ++i) tma_load_2d(smem + (uint32_t)i * sbytes + 128 * KB, &tmX, (kb0 + i) * KB, t0, &full[i]);
+    __syncwarp();
+    RingPos r;  // the stage of load npre + j is that of load j
+    int it = npre;
+    if (npre == p.stages)
+      for (; it < nkb; ++it, r.next(p.stages)) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[r.st], r.ph, a.err.wait_ns))) {
+          s_flag[0] = 1;
+          set_error(a.err, DEV_TIMEOUT);
+          break;
+        }
+        uint8_t* s = smem + (uint32_t)r.st * sbytes;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&full[r.st], tx);
+          tma_load_2d(s, &tmW, (kb0 + it) * KB, f0, &full[r.st]);
+          tma_load_2d(s + 128 * KB, &tmX, (kb0 + it) * KB, t0, &full[r.st]);
+        }
+        __syncwarp();
+      }
+    if (lane == 0)
+      for (int i = it > p.stages ? it - p.stages : 0; i < it; ++i)
+        if (!mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kDrainNs)) set_error(a.err, DEV_DRAIN);
+  } else if (warp == 1) {
     const uint32_t idesc = idesc_i8(128, p.tn);
-    for (int it = 0; it < nkb; ++it) {
-      const int st = it % p.stages;
-      if (!mbar_wait(&full[st], (it / p.stages) & 1, a.err.wait_ns)) {
+    const uint64_t a0 = sw128_desc(smem_u32(smem), 16, 1024), b0 = sw128_desc(smem_u32(smem) + 128 * KB, 16, 1024);
+    RingPos r;
+    for (int it = 0; it < nkb; ++it, r.next(p.stages)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[r.st], r.ph, a.err.wait_ns))) {
         s_flag[0] = 1;
         set_error(a.err, DEV_TIMEOUT);
         break;
       }
       tc_fence_after();
-      const uint32_t sa = smem_u32(smem + (size_t)st * sbytes);
-      const uint64_t ad = sw128_desc(sa, 16, 1024), bd = sw128_desc(sa + 128 * KB, 16, 1024);
+      const uint64_t ad = desc_add(a0, (uint32_t)r.st * sbytes), bd = desc_add(b0, (uint32_t)r.st * sbytes);
+      if (elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < KB / 32; ++kk)
-        umma_i8(tmem, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, (it | kk) != 0 ? 1u : 0u);
-      umma_commit(&empty[st]);
+        for (int kk = 0; kk < KB / 32; ++kk)
+          umma_i8(tmem, desc_add(ad, kk * 32u), desc_add(bd, kk * 32u), idesc, (it | kk) != 0 ? 1u : 0u);
+        umma_commit(&empty[r.st]);
+      }
+      __syncwarp();
     }
-    umma_commit(acc_full);  // always issued, so the epilogue's wait ends
+    if (elect_one()) umma_commit(acc_full);  // always issued, so the epilogue's wait ends
   }
   __syncwarp();
   pdl_wait();
