@@ -68,6 +68,15 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
 }
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%6, %7};\n\t"
+      "fma.rn.f32x2 c, a, b, d;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -81,7 +90,21 @@ __device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// AND over the 128 threads of the four warps that share 32 rows.
+// OR over the 128 threads of the four warps that share 32 rows.
+__device__ __forceinline__ bool rows_or(int id, bool v) {
+  __syncwarp();
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id)
+      : "memory");
+  return r != 0;
+}
+// AND over them.
 __device__ __forceinline__ bool rows_and(int id, bool v) {
   __syncwarp();
   uint32_t r;
@@ -144,7 +167,7 @@ struct Smem {
   static constexpr uint32_t kTile = CK * D * 2;  // one chunk of K (or V) in bf16
   static constexpr uint32_t q = 0, k = QROWS * D * 2, v = k + 2 * kTile, sc = v + 2 * kTile;
   static constexpr uint32_t pm = sc + 2 * 2 * CK * 4;    // scales: 2 chunks of [ks 64 | vs 64]
-  static constexpr uint32_t l = pm + 2 * 4 * QROWS * 4;  // partial maxima [2][4][128]
+  static constexpr uint32_t l = pm + 4 * QROWS * 4;      // partial maxima [4][128]
   static constexpr uint32_t bar = l + 4 * QROWS * 4;     // partial sums [4][128]
   static constexpr uint32_t total = bar + 256 + 1024;
 };
@@ -422,8 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     const int rq = qt * QROWS + r;
     const int oc0 = part * (D / 4);
     const int lim = a.causal ? min(len, len - a.n_q + 1 + min(rq, rows - 1) / a.group) : len;
-    float m_run = -INFINITY, l_run = 0.f;
-    bool ok = true;
+    float ref = 0.f, l_run = 0.f;  // reference in the log2 domain; has: some key was visible
+    bool ok = true, has = false;
     for (int i = 0; i < nch; ++i) {
       const int st = i & 1, c = c0 + i;
       const bool got = mbar_wait(&sc_full[st], (i >> 1) & 1, a.err.wait_ns) &&
@@ -437,12 +460,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       const float* sc = s_sc + st * 2 * CK + part * KP;
       // visible keys of this part's
       const int vis = (c < nc ? lim - c * CK : a.n_new - (c - nc) * CK) - part * KP;
+      // Scores in units of the row's reference: y = s ks - ref.  The reference
+      // (a running maximum) moves only when a score exceeds it by more than 8, a
+      // factor 256, so that O is rescaled rarely; until then no part needs
+      // another part's maximum, only everyone's word that it stays.
       float2* s2 = reinterpret_cast<float2*>(sv);
+      const float2 nref = make_float2(-ref, -ref);
 #pragma unroll
       for (int j = 0; j < KP / 2; j += 2) {
         const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * j);
-        s2[j] = mul2(s2[j], make_float2(k4.x, k4.y));
-        s2[j + 1] = mul2(s2[j + 1], make_float2(k4.z, k4.w));
+        s2[j] = fma2(s2[j], make_float2(k4.x, k4.y), nref);
+        s2[j + 1] = fma2(s2[j + 1], make_float2(k4.z, k4.w), nref);
       }
       if (vis < KP) {
 #pragma unroll
@@ -451,31 +479,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       float mt[KP / 4];
 #pragma unroll
       for (int j = 0; j < KP / 4; ++j) mt[j] = fmaxf(max3(sv[4 * j], sv[4 * j + 1], sv[4 * j + 2]), sv[4 * j + 3]);
-      float* pm = s_pm + st * 4 * QROWS + r;
-      pm[part * QROWS] = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]);
-      // every part of the row has its scores in registers (P overwrites S) and
-      // its maximum in place, and all go on or stop together
-      if (!rows_and(1 + (warp & 3), got && s_flag[0] == 0)) {
-        ok = false;
-        break;
+      const float pmax = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]);
+      // Every part of the rows has its scores in registers (P overwrites S).
+      // A part that must stop asks for a move too, so all meet below.
+      const bool mine = got && s_flag[0] == 0;
+      float alpha = 1.f;
+      if (rows_or(1 + (warp & 3), !mine || (has ? pmax > 8.f : pmax != -INFINITY))) {
+        float* pm = s_pm + r;
+        pm[part * QROWS] = pmax;
+        if (!rows_and(1 + (warp & 3), mine)) {
+          ok = false;
+          break;
+        }
+        const float cmax = fmaxf(max3(pm[0], pm[QROWS], pm[2 * QROWS]), pm[3 * QROWS]);
+        const bool move = has ? cmax > 8.f : cmax != -INFINITY;  // (NaN alone: the reference stays)
+        const float up = move && cmax == cmax ? cmax : 0.f;
+        ref += up;
+        alpha = has ? ex2(-up) : 1.f;
+        has = has || move;
+        const float2 nup = make_float2(-up, -up);
+#pragma unroll
+        for (int j = 0; j < KP / 2; ++j) s2[j] = add2(s2[j], nup);
+        rows_and(1 + (warp & 3), true);  // the maxima are read: the next move may write them
       }
-      const float cmax = fmaxf(max3(pm[0], pm[QROWS], pm[2 * QROWS]), pm[3 * QROWS]);
-      const float mx = cmax > m_run + 8.f ? cmax : m_run;
-      const float ref = mx == -INFINITY ? 0.f : mx;  // no visible key so far
-      const float alpha = ex2(m_run - ref);          // 1 when unchanged, 0 at first
-      const float2 nref = make_float2(-ref, -ref);
       float2 sum[2];
 #pragma unroll
       for (int j = 0; j < KP / 2; ++j) {
-        s2[j] = add2(s2[j], nref);
         s2[j].x = ex2(s2[j].x);
         s2[j].y = ex2(s2[j].y);
         sum[j & 1] = j < 2 ? s2[j] : add2(sum[j & 1], s2[j]);
       }
       sum[0] = add2(sum[0], sum[1]);
-      l_run = l_run * (m_run == -INFINITY ? 1.f : alpha) + (sum[0].x + sum[0].y);
-      const bool scale_o = i > 0 && alpha != 1.f && m_run != -INFINITY;
-      m_run = mx;
+      l_run = l_run * alpha + (sum[0].x + sum[0].y);
+      const bool scale_o = i > 0 && alpha != 1.f;
 #pragma unroll
       for (int j = 0; j < KP / 2; j += 2) {
         const float4 v4 = *reinterpret_cast<const float4*>(sc + CK + 2 * j);
@@ -520,16 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     ok = rows_and(1 + (warp & 3), ok && s_flag[0] == 0);
     tc_fence_after();
     const float l = ((s_l[r] + s_l[QROWS + r]) + s_l[2 * QROWS + r]) + s_l[3 * QROWS + r];
-    // NaN scores alone leave the maximum at -inf: the row is not empty
-    if (m_run == -INFINITY && l != 0.f) m_run = 0.f;
     // Output rows go through shared memory (every MMA is done: the tiles are
     // free), so that a row leaves as one run of 16-byte stores; straight from
     // the registers, a warp's store touches 32 rows and the 128 rows of a tile
     // took 7000 cycles.  Chunks of 16 bytes are swizzled by the row.
     const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
-    const bool some = ok && nch > 0 && m_run != -INFINITY;
+    const bool some = ok && nch > 0 && l != 0.f;  // (NaN counts)
     const size_t pr0 = ((size_t)bg * splits + split) * ((size_t)gridDim.x * QROWS) + qt * QROWS;
-    if (splits > 1 && part == 0) a.part_ml[pr0 + r] = some ? make_float2(m_run, l) : make_float2(-INFINITY, 0.f);
+    if (splits > 1 && part == 0) a.part_ml[pr0 + r] = some ? make_float2(ref, l) : make_float2(-INFINITY, 0.f);
     const uint32_t stage = smem_u32(smem);
     const int esz = splits == 1 ? 2 : 4;
     const uint32_t rowb = (uint32_t)(D * esz), srow = stage + (uint32_t)r * rowb;

@@ -21,26 +21,34 @@ _CODES = {torch.float32: 0, torch.bfloat16: 1}  # PAE_FP32, PAE_BF16
 _QUERY = struct.Struct("5P12q5if")  # pae_kv8_query
 _PAIR = struct.Struct("2q").pack
 _raw_stream = torch._C._cuda_getCurrentRawStream
-_functions: dict = {}
+_current_device = torch._C._cuda_getDevice
+_int8, _int32, _float32, _bfloat16 = torch.int8, torch.int32, torch.float32, torch.bfloat16
 
 
-def _function(name: str, argtypes: str):
-    """libpae's `name` with c_void_p (p), c_int (i), c_longlong (q), c_size_t
-    (z) or c_float (f) arguments: bytes pass as pointers."""
-    f = _functions.get(name)
-    if f is None:
+class _Library:
+    """libpae's functions with c_void_p (p), c_int (i), c_longlong (q),
+    c_size_t (z) or c_float (f) arguments (bytes pass as pointers), looked up
+    on first use."""
+
+    _types = {"pae_quantize_rows": "pqiiifppp", "pae_linear_i8": "ppppiiipqip", "pae_kv8_write": "pppppppiiip",
+              "pae_kv8_read": "pppppppiiip", "pae_kv8_attention": "pppzp"}
+
+    def __getattr__(self, name):
         import ctypes
         kinds = {"p": ctypes.c_void_p, "i": ctypes.c_int, "q": ctypes.c_longlong, "z": ctypes.c_size_t, "f": ctypes.c_float}
         f = _fm.lib()[name]  # an object of its own: the package's prototype stays
         f.restype = ctypes.c_int
-        f.argtypes = [kinds[c] for c in argtypes]
-        _functions[name] = f
-    return f
+        f.argtypes = [kinds[c] for c in self._types[name]]
+        setattr(self, name, f)
+        return f
+
+
+_lib = _Library()
 
 
 def _call(device: int, f, *args) -> None:
     """f(*args, stream) on the device's current stream, with the device current."""
-    if device == torch.cuda.current_device():
+    if device == _current_device():
         status = f(*args, _raw_stream(device))
     else:
         with torch.cuda.device(device):
@@ -68,7 +76,7 @@ def _dtype_code(dtype: torch.dtype, what: str) -> int:
 
 
 def _check_vector(t: torch.Tensor, n: int, dtype: torch.dtype, what: str) -> None:
-    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}")
 
 
@@ -76,9 +84,11 @@ def quantize_rows(x: torch.Tensor, rms_eps: Optional[float] = None) -> Tuple[tor
     """x [rows, width] (float32 or bfloat16, unit stride along width) ->
     (codes int8 [rows, width], scale float32 [rows]).  rms_eps: quantise the
     RMSNorm x / sqrt(mean(x^2) + rms_eps) of each row instead of x."""
-    if x.dim() != 2 or x.shape[1] < 1:
-        raise ValueError("x must be [rows, width] with width >= 1")
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
     rows, width = x.shape
+    if width < 1:
+        raise ValueError("x must have width >= 1")
     ldx, unit = x.stride()
     if unit != 1 and width > 1:
         raise ValueError("x must be contiguous along width")
@@ -86,9 +96,9 @@ def quantize_rows(x: torch.Tensor, rms_eps: Optional[float] = None) -> Tuple[tor
     if rms_eps is not None and not rms_eps > 0:
         raise ValueError("rms_eps must be positive")
     device = _check_device(x)
-    codes = x.new_empty((rows, width), dtype=torch.int8)
-    scale = x.new_empty((rows,), dtype=torch.float32)
-    _call(device, _function("pae_quantize_rows", "pqiiifppp"), x.data_ptr(), ldx if rows > 1 else width, rows, width,
+    codes = x.new_empty((rows, width), dtype=_int8)
+    scale = x.new_empty((rows,), dtype=_float32)
+    _call(device, _lib.pae_quantize_rows, x.data_ptr(), ldx if rows > 1 else width, rows, width,
           code, rms_eps or 0.0, codes.data_ptr(), scale.data_ptr())
     return codes, scale
 
@@ -97,23 +107,25 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
               out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """(x [tokens, k] int8 times w [n, k] int8 transposed) * x_scale[token] *
     w_scale[channel] -> [tokens, n] in out_dtype (or into `out`)."""
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x must be [tokens, k] and w [n, k]")
+    tokens, k = x.shape
+    n, kw = w.shape
+    if k != kw:
         raise ValueError("x [tokens, k] and w [n, k] must share k")
-    if x.dtype != torch.int8 or w.dtype != torch.int8:
+    if x.dtype != _int8 or w.dtype != _int8:
         raise ValueError("x and w must be int8 codes")
     if not (x.is_contiguous() and w.is_contiguous()):
         raise ValueError("x and w must be contiguous")
-    tokens, k = x.shape
-    n = w.shape[0]
-    _check_vector(x_scale, tokens, torch.float32, "x_scale")
-    _check_vector(w_scale, n, torch.float32, "w_scale")
+    _check_vector(x_scale, tokens, _float32, "x_scale")
+    _check_vector(w_scale, n, _float32, "w_scale")
     device = _check_device(x, x_scale, w, w_scale, out)
     if out is None:
         out = x.new_empty((tokens, n), dtype=out_dtype)
     elif out.shape != (tokens, n) or (out.stride(1) != 1 and n > 1):
         raise ValueError("out must be [tokens, n], contiguous along n")
     code = _dtype_code(out.dtype, "out")
-    _call(device, _function("pae_linear_i8", "ppppiiipqip"), x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
+    _call(device, _lib.pae_linear_i8, x.data_ptr(), x_scale.data_ptr(), w.data_ptr(),
           w_scale.data_ptr(), tokens, n, k, out.data_ptr(), out.stride(0) if tokens > 1 else n, code)
     return out
 
@@ -152,10 +164,10 @@ class KvCacheInt8:
         cu = at = None
         if cu_rows is not None:
             n_seq = cu_rows.shape[0] - 1
-            _check_vector(cu_rows, n_seq + 1, torch.int32, "cu_rows")
+            _check_vector(cu_rows, n_seq + 1, _int32, "cu_rows")
             cu = cu_rows.data_ptr()
         if start is not None:
-            _check_vector(start, n_seq, torch.int32, "start")
+            _check_vector(start, n_seq, _int32, "start")
             at = start.data_ptr()
         return n_seq, cu, at
 
@@ -177,7 +189,7 @@ class KvCacheInt8:
         ks, vs = self._strides(k, "k"), self._strides(v, "v")
         n_seq, cu, at = self._seqs(cu_rows, start)
         device = _check_device(self.k, k, v, cu_rows, start)
-        _call(device, _function("pae_kv8_write", "pppppppiiip"), self._p, k.data_ptr(), v.data_ptr(), ks, vs, cu, at,
+        _call(device, _lib.pae_kv8_write, self._p, k.data_ptr(), v.data_ptr(), ks, vs, cu, at,
               n_seq, k.shape[0], code)
 
     def read(self, cu_rows: Optional[torch.Tensor], start: Optional[torch.Tensor], n_rows: int,
@@ -189,7 +201,7 @@ class KvCacheInt8:
         device = _check_device(self.k, cu_rows, start)
         shape = (n_rows, self.shape[1], self.shape[3])
         k, v = self.k.new_empty(shape, dtype=dtype), self.k.new_empty(shape, dtype=dtype)
-        _call(device, _function("pae_kv8_read", "pppppppiiip"), self._p, k.data_ptr(), v.data_ptr(), None, None, cu, at,
+        _call(device, _lib.pae_kv8_read, self._p, k.data_ptr(), v.data_ptr(), None, None, cu, at,
               n_seq, n_rows, code)
         return k, v
 
@@ -201,7 +213,7 @@ class KvCacheInt8:
         return Kv8Plan((n_seq, n_q, n_q_heads, fresh), ws, self.k.get_device())
 
     def _rows(self, t: torch.Tensor, heads: int, what: str) -> Tuple[int, int, int]:
-        if t.dim() != 4 or t.dtype != torch.bfloat16 or t.shape[2] != heads or t.shape[3] != self.shape[3] or t.stride(3) != 1:
+        if t.dim() != 4 or t.dtype != _bfloat16 or t.shape[2] != heads or t.shape[3] != self.shape[3] or t.stride(3) != 1:
             raise ValueError(f"{what} must be bfloat16 [n_seq, n, {heads}, {self.shape[3]}], contiguous along the last dimension")
         n0, n1, n2, _ = t.shape
         s0, s1, s2, _ = t.stride()
@@ -223,7 +235,7 @@ class KvCacheInt8:
         if (k_new is None) != (v_new is None):
             raise ValueError("k_new and v_new go together")
         device = _check_device(self.k, q, lens, k_new, v_new, out)
-        _check_vector(lens, n_seq, torch.int32, "lens")
+        _check_vector(lens, n_seq, _int32, "lens")
         qs = self._rows(q, hq, "q")
         n_new, kp, vp, ks, vs = 0, 0, 0, (0, 0, 0), (0, 0, 0)
         if k_new is not None:
@@ -245,7 +257,7 @@ class KvCacheInt8:
         query = _QUERY.pack(lens.data_ptr(), q.data_ptr(), out.data_ptr(), kp, vp, *qs, *os, *ks, *vs, n_seq, n_q, hq,
                             n_new, 1 if causal else 0, scale or 0.0)
         ws = plan.workspace
-        _call(device, _function("pae_kv8_attention", "pppzp"), self._p, query, None if ws is None else ws.data_ptr(),
+        _call(device, _lib.pae_kv8_attention, self._p, query, None if ws is None else ws.data_ptr(),
               plan.bytes)
         return out
 
