@@ -10,8 +10,11 @@
 //                         bf16 integers (exact) in the 128-byte swizzled tiles
 //                         the MMA reads; fresh keys and values are copied as
 //                         they are
-//   MMA thread            S = Q K^T (128 x 64, double-buffered in TMEM), then
-//                         O += P V (P read from TMEM, V read MN-major)
+//   two MMA warps         S = Q K^T (128 x 64, double-buffered in TMEM) and
+//                         O += P V (P read from TMEM, V read MN-major): an
+//                         issuing warp gets one instruction in thirty cycles
+//                         or so beside the others, and one warp for both was
+//                         part of the chunk-to-chunk chain
 //   scale warp            the chunk's key and value scales
 //   softmax (16 warps)    four threads per row: scores x key scale, online
 //                         softmax in the log2 domain (O is rescaled only when
@@ -33,7 +36,7 @@ namespace {
 constexpr int QROWS = 128, CK = 64;
 constexpr int kSmxWarps = 16;              // softmax warps (0-15): four threads per row
 constexpr int kSmx = kSmxWarps * 32;
-constexpr int kMmaWarp = kSmxWarps, kScaleWarp = kMmaWarp + 1, kConvWarp = kScaleWarp + 1;
+constexpr int kMmaWarp = kSmxWarps, kPvWarp = kMmaWarp + 1, kScaleWarp = kMmaWarp + 2, kConvWarp = kMmaWarp + 3;
 constexpr int kConv = 128;                 // converter threads per operand
 constexpr int kThreads = kConvWarp * 32 + 2 * kConv;
 constexpr int KP = CK / 4;                 // keys per softmax part
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   uint64_t* p_full = bars + 11;     // [2] P written over S
   uint64_t* o_done = bars + 13;     // [2] PV of the buffer's chunk done
   uint64_t* sc_full = bars + 15;    // [2] the chunk's scales in place
-  uint64_t* drain = bars + 17;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* drain = bars + 17;      // [2] one per MMA warp
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 19);
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* s_sc = reinterpret_cast<float*>(smem + L::sc);
   float* s_pm = reinterpret_cast<float*>(smem + L::pm);
@@ -214,7 +217,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       mbar_init(&o_done[i], 1);
       mbar_init(&sc_full[i], 32);
     }
-    mbar_init(drain, 1);
+    mbar_init(&drain[0], 1);
+    mbar_init(&drain[1], 1);
     s_flag[0] = 0;
     fence_mbar_init();
   }
@@ -350,67 +354,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       mbar_arrive(&sc_full[slot]);
       if (i + 1 < nch) load(c0 + i + 1);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ------------------------------------------------------------------- MMA
-    // The whole warp walks the loop and one lane issues: addresses then live in
-    // uniform registers.  (Issued from a one-lane branch, the 20 MMAs of a chunk
-    // took 1900 cycles of a scheduler that six other warps keep busy.)
+    // A whole warp walks the loop and one lane issues (the same one each time):
+    // addresses then live in uniform registers.  Issued from a one-lane branch,
+    // the 20 MMAs of a chunk took 1900 cycles.
     if (nch > 0) {
-      constexpr uint32_t idesc_s = idesc_bf16(QROWS, CK), idesc_o = idesc_bf16(QROWS, D, 0, 1);
-      bool good = mbar_wait(q_full, 0, a.err.wait_ns);
-      const uint64_t q_desc = sw128_desc(smem_u32(smem + L::q), 16, 1024);
-      const uint64_t k_desc = sw128_desc(smem_u32(smem + L::k), 16, 1024);
-      const uint64_t v_desc = sw128_desc(smem_u32(smem + L::v), CK * 128, 1024);
-      const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, v_lo = (uint32_t)v_desc;
-      const uint32_t qk_hi = (uint32_t)(q_desc >> 32), v_hi = (uint32_t)(v_desc >> 32);
-      // S of chunk i goes over P of chunk i - 2: that chunk's PV must be done
-      auto issue_s = [&](int i) -> bool {
-        const int st = i & 1;
-        bool ok = mbar_wait(&k_full[st], (i >> 1) & 1, a.err.wait_ns);
-        if (ok && i >= 2) ok = mbar_wait(&o_done[st], ((i >> 1) & 1) ^ 1, a.err.wait_ns);
-        if (!__all_sync(0xffffffffu, ok)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(st * CK), kl = k_lo + (uint32_t)st * (L::kTile >> 4);
-        if (elect_one()) {
-          mma_ss<false>(d, q_lo, kl, qk_hi, idesc_s);
+      bool good = true;
+      if (warp == kMmaWarp) {
+        constexpr uint32_t idesc_s = idesc_bf16(QROWS, CK);
+        const uint64_t q_desc = sw128_desc(smem_u32(smem + L::q), 16, 1024);
+        const uint64_t k_desc = sw128_desc(smem_u32(smem + L::k), 16, 1024);
+        const uint32_t q_lo = (uint32_t)q_desc, k_lo = (uint32_t)k_desc, hi = (uint32_t)(q_desc >> 32);
+        good = __all_sync(0xffffffffu, mbar_wait(q_full, 0, a.err.wait_ns));
+        for (int i = 0; good && i < nch; ++i) {
+          const int st = i & 1;
+          // S of chunk i goes over P of chunk i - 2: that chunk's PV must be done
+          good = mbar_wait(&k_full[st], (i >> 1) & 1, a.err.wait_ns) &&
+                 (i < 2 || mbar_wait(&o_done[st], ((i >> 1) & 1) ^ 1, a.err.wait_ns));
+          if (!(good = __all_sync(0xffffffffu, good))) break;
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(st * CK), kl = k_lo + (uint32_t)st * (L::kTile >> 4);
+          if (elect_one()) {
+            mma_ss<false>(d, q_lo, kl, hi, idesc_s);
 #pragma unroll
-          for (uint32_t k16 = 1; k16 < D / 16; ++k16) {
-            const uint32_t x = k16 >> 2, w = (k16 & 3u) * 32u;
-            mma_ss<true>(d, q_lo + ((x * QROWS * 128u + w) >> 4), kl + ((x * CK * 128u + w) >> 4), qk_hi, idesc_s);
+            for (uint32_t k16 = 1; k16 < D / 16; ++k16) {
+              const uint32_t x = k16 >> 2, w = (k16 & 3u) * 32u;
+              mma_ss<true>(d, q_lo + ((x * QROWS * 128u + w) >> 4), kl + ((x * CK * 128u + w) >> 4), hi, idesc_s);
+            }
+            umma_commit(&s_full[st]);
+            umma_commit(&k_empty[st]);
           }
-          umma_commit(&s_full[st]);
-          umma_commit(&k_empty[st]);
+          __syncwarp();
         }
-        __syncwarp();
-        return true;
-      };
-      good = __all_sync(0xffffffffu, good);
-      if (good) good = issue_s(0);
-      for (int i = 0; good && i < nch; ++i) {
-        const int st = i & 1;
-        if (i + 1 < nch && !(good = issue_s(i + 1))) break;
-        good = mbar_wait(&p_full[st], (i >> 1) & 1, a.err.wait_ns) && mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns);
-        if (!(good = __all_sync(0xffffffffu, good))) break;
-        tc_fence_after();
-        const uint32_t p = tmem + (uint32_t)(st * CK), vl = v_lo + (uint32_t)st * (L::kTile >> 4);
-        if (elect_one()) {
-          mma_ts(t_o, p, vl, v_hi, idesc_o, i > 0 ? 1u : 0u);
+      } else {
+        constexpr uint32_t idesc_o = idesc_bf16(QROWS, D, 0, 1);
+        const uint64_t v_desc = sw128_desc(smem_u32(smem + L::v), CK * 128, 1024);
+        const uint32_t v_lo = (uint32_t)v_desc, hi = (uint32_t)(v_desc >> 32);
+        for (int i = 0; good && i < nch; ++i) {
+          const int st = i & 1;
+          good = mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns) && mbar_wait(&p_full[st], (i >> 1) & 1, a.err.wait_ns);
+          if (!(good = __all_sync(0xffffffffu, good))) break;
+          tc_fence_after();
+          const uint32_t p = tmem + (uint32_t)(st * CK), vl = v_lo + (uint32_t)st * (L::kTile >> 4);
+          if (elect_one()) {
+            mma_ts(t_o, p, vl, hi, idesc_o, i > 0 ? 1u : 0u);
 #pragma unroll
-          for (uint32_t k16 = 1; k16 < CK / 16; ++k16) mma_ts(t_o, p + k16 * 8u, vl + ((k16 * 16u * 128u) >> 4), v_hi, idesc_o, 1u);
-          umma_commit(&o_done[st]);
-          umma_commit(&v_empty[st]);
+            for (uint32_t k16 = 1; k16 < CK / 16; ++k16) mma_ts(t_o, p + k16 * 8u, vl + ((k16 * 16u * 128u) >> 4), hi, idesc_o, 1u);
+            umma_commit(&o_done[st]);
+            umma_commit(&v_empty[st]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       if (!good) {
         s_flag[0] = 1;
         set_error(a.err, DEV_TIMEOUT);
       }
-      // every MMA issued must finish before TMEM is freed (the commits come from
-      // whichever lane was elected: one of the warp's, the same each time)
+      // every MMA issued must finish before TMEM is freed
       if (elect_one()) {
-        umma_commit(drain);
-        if (!mbar_wait(drain, 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
+        umma_commit(&drain[warp - kMmaWarp]);
+        if (!mbar_wait(&drain[warp - kMmaWarp], 0, kDrainNs)) set_error(a.err, DEV_DRAIN);
       }
     }
     __syncwarp();
