@@ -93,10 +93,15 @@ struct Kv8AttnArgs {
   int n_seq, n_q, n_new, group;  // group = query heads per KV head
   int causal;
   float scale_log2;         // softmax scale x log2(e)
-  float* part_o;            // unnormalised rows: tc [n_seq * heads][splits][rows][d], else [blocks][2][8][d]
-  float2* part_ml;          // their (max in the log2 domain, sum)
+  float* part_o;            // averages over the part's keys: tc [n_seq * heads][splits][rows][d], else [blocks][2][8][d]
+  float2* part_ml;          // their weights as (log2, 1), see part_weight
   DevErr err;
 };
+// A part's weight, the log2 of its row sum, as a maximum and a sum for the
+// merge: (-inf, 0) where the row saw no key, (0, NaN) where its scores are NaN.
+__device__ __forceinline__ float2 part_weight(float lw) {
+  return lw == -INFINITY ? make_float2(lw, 0.f) : lw == lw ? make_float2(lw, 1.f) : make_float2(0.f, lw);
+}
 // Place the partial rows and their statistics in a workspace of p.ws_bytes.
 inline void kv8_attn_parts(Kv8AttnArgs* a, const Kv8AttnPlan& p, void* workspace) {
   a->part_o = static_cast<float*>(workspace);

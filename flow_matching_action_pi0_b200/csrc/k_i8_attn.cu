@@ -9,10 +9,16 @@
 // lo) qs with two signed 8-bit digits, |q| error at most max|q| 2^-16, so the
 // key codes go into integer products as they lie in memory, two per 32
 // channels, and the sums are exact.  (As bf16 operands every pair of codes
-// costs four instructions, half of the loop.)  Values: the codes become bf16
-// integers, which is exact, and the value's scale multiplies its probability
-// (rounded once to bf16, as an attention with bf16 values rounds its
-// probabilities).
+// costs four instructions, half of the loop.)  Values: the codes become fp16
+// integers, exactly, and the value's scale joins the exponent:
+//   c_j = exp2(s_j + log2 vs_j - ref) = p_j vs_j 2^(m - ref),
+// so that c in fp16 (rounded once, to 11 bits) is in units of the row's largest
+// contribution whatever the scales are: max c lies in [1, 256], and what falls
+// under fp16's 2^-24 is less than the largest one's own code step by far.  The
+// row sums have a reference m of their own, since a key may weigh much and
+// carry little: sum p_j in fp32, lane by lane.  The two meet in the exponent of
+// the row's last factor, 2^(ref - m) / sum, and partial rows are parked as
+// averages with the logarithm of their weight, so no size of V overflows.
 //
 // Bound: bytes of the cache (2 (d + 4) per key and KV head).  The G query
 // heads of a KV head share every byte, 8 rows at a time as the N side of
@@ -40,6 +46,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include <cuda_fp16.h>
+
 #include "int8.h"
 #include "launch.cuh"
 
@@ -56,9 +64,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ void mma_bf16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -79,15 +87,18 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
 }
 
 // Two signed bytes in bits 0-7 and 16-23 of w (the other bits are ignored) ->
-// bf16x2, exactly: with v the low 7 bits and s the sign bit, 0x4300 | v is
-// 128 + v and 0x4300 | s << 7 is 128 (1 + s); their difference is v - 128 s.
-__device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
-  const uint32_t a = (w & 0x007F007Fu) | 0x43004300u;
-  const uint32_t b = (w & 0x00800080u) | 0x43004300u;
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+// fp16x2, exactly: 0x6400 | (byte ^ 0x80) is 1024 + 128 + code.
+__device__ __forceinline__ uint32_t bytes_f16x2(uint32_t w) {
+  const uint32_t u = (w & 0x00FF00FFu) ^ 0x64806480u;
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1152.f, 1152.f));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;  // one instruction for the pair, round to nearest even
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -154,7 +165,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
   constexpr int VM = VB / 2;                 // products per block
   constexpr int STEP = kUnit;
   extern __shared__ __align__(16) float s_o[];  // the warps' rings; at the end of a sequence [kWarps][8][D + 4]
-  __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+  __shared__ float s_m[kWarps][8], s_x[kWarps][8], s_l[kWarps][8];
   __shared__ float2 s_row[8];
   __shared__ uint64_t s_bar[kWarps][kStages];
   __shared__ long long s_scan[kWarps];
@@ -305,7 +316,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     for (int m = 0; m < VM; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][m][j] = 0.f;
-  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+  float m_run[2] = {-INFINITY, -INFINITY};                      // reference of c, the warp's
+  float x_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};  // of the sum, this lane's
 
   for (; at < key1; at += STEP) {
     const float sc = sc_next[0];
@@ -329,22 +341,42 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       mma_s8(ch, x0.z, x1.z, x0.w, x1.w, qh[j][2], qh[j][3]);
       mma_s8(cl, x0.z, x1.z, x0.w, x1.w, ql[j][2], ql[j][3]);
     }
-    float ks[2], vs[2];
+    const float lv_l = __log2f(sc);  // (of the V scales, lanes 16-31; 0, with codes 0, gives -inf)
+    float ks[2], lv[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       ks[i] = __shfl_sync(0xFFFFFFFFu, sc, g + 8 * i);
-      vs[i] = __shfl_sync(0xFFFFFFFFu, sc, 16 + g + 8 * i);
+      lv[i] = __shfl_sync(0xFFFFFFFFu, lv_l, 16 + g + 8 * i);
     }
     float c[4];  // (|256 hi + lo| < 2^31: 127 * 127 * 256 * 257)
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = (float)(ch[i] * 256 + cl[i]) * qs[i & 1];
-    const float v0 = vs[0], v1 = vs[1];
     const int ka = at + g, kc = ka + 8;
-    float x[4];
-    x[0] = ka < min(lim[0], key1) ? c[0] * ks[0] : -INFINITY;
-    x[1] = ka < min(lim[1], key1) ? c[1] * ks[0] : -INFINITY;
-    x[2] = kc < min(lim[0], key1) ? c[2] * ks[1] : -INFINITY;
-    x[3] = kc < min(lim[1], key1) ? c[3] * ks[1] : -INFINITY;
+    const bool in[4] = {ka < min(lim[0], key1), ka < min(lim[1], key1), kc < min(lim[0], key1), kc < min(lim[1], key1)};
+    float x[4];  // masked places: -inf, whatever their scale is
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = in[i] ? c[i] * ks[i >> 1] : -INFINITY;
+    // The sum's reference moves when a score exceeds it by 64: fp32 holds both
+    // sides, and what is under 2^-126 of it is nothing beside the maximum.
+    bool far[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) far[i] = fmaxf(x[i], x[i + 2]) > x_run[i] + 64.f;
+    if (__any_sync(0xFFFFFFFFu, far[0] || far[1])) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!far[i]) continue;
+        const float nx = fmaxf(x[i], x[i + 2]);
+        l_run[i] *= ex2(x_run[i] - nx);
+        x_run[i] = nx;
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = x[i] == -INFINITY ? 0.f : ex2(x[i] - x_run[i & 1]);
+    l_run[0] += p[0] + p[2];
+    l_run[1] += p[1] + p[3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = in[i] ? x[i] + lv[i >> 1] : -INFINITY;
     float al[2];
     bool grow = false;
 #pragma unroll
@@ -354,18 +386,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
       // the reference moves only when the maximum grows by more than 8 (a
-      // factor 256): probabilities stay below 256 and O is rescaled rarely
+      // factor 256): c stays below 256 and O is rescaled rarely
       const bool up = mx > m_run[i] + 8.f || m_run[i] == -INFINITY;
       const float nm = up ? fmaxf(mx, m_run[i]) : m_run[i];
       al[i] = nm == -INFINITY ? 1.f : ex2(m_run[i] - nm);
       grow |= al[i] != 1.f;
       m_run[i] = nm;
     }
-    float p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = x[i] == -INFINITY ? 0.f : ex2(x[i] - m_run[i & 1]);
-    l_run[0] = l_run[0] * al[0] + (p[0] + p[2]);
-    l_run[1] = l_run[1] * al[1] + (p[1] + p[3]);
     if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
       for (int i = 0; i < VBLK; ++i)
@@ -377,10 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
           o[i][m][3] *= al[1];
         }
     }
-    // P times the value scales; masked places stay 0 whatever their scale is
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = x[i] == -INFINITY ? 0.f : p[i] * (i < 2 ? v0 : v1);
-    const uint32_t b0 = movmatrix(pack_bf16(p[0], p[1])), b1 = movmatrix(pack_bf16(p[2], p[3]));
+    const uint32_t b0 = movmatrix(pack_f16(p[0], p[1])), b1 = movmatrix(pack_f16(p[2], p[3]));
 #pragma unroll
     for (int j = 0; j < VBLK; ++j) {
       uint32_t vr[4][VB / 4];
@@ -399,11 +425,11 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       for (int m = 0; m < VM; ++m) {
         const int w = m >> 1;
         const uint32_t lo = (m & 1) ? 0x0602u : 0x0400u, hi = (m & 1) ? 0x0703u : 0x0501u;
-        const uint32_t f[4] = {bytes_bf16x2(__byte_perm(vr[0][w], vr[1][w], lo)),
-                               bytes_bf16x2(__byte_perm(vr[0][w], vr[1][w], hi)),
-                               bytes_bf16x2(__byte_perm(vr[2][w], vr[3][w], lo)),
-                               bytes_bf16x2(__byte_perm(vr[2][w], vr[3][w], hi))};
-        mma_bf16(o[j][m], f, b0, b1);
+        const uint32_t f[4] = {bytes_f16x2(__byte_perm(vr[0][w], vr[1][w], lo)),
+                               bytes_f16x2(__byte_perm(vr[0][w], vr[1][w], hi)),
+                               bytes_f16x2(__byte_perm(vr[2][w], vr[3][w], lo)),
+                               bytes_f16x2(__byte_perm(vr[2][w], vr[3][w], hi))};
+        mma_f16(o[j][m], f, b0, b1);
       }
     }
     __syncwarp();  // every lane has read the stage: the next copy may overwrite it
@@ -414,17 +440,20 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     ++cur;
   }
 
-  // row sums over the 8 lanes that share t
+  // row sums over the 8 lanes that share t, in units of their largest reference
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    float l = l_run[i];
+    float mx = x_run[i];
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+    float l = x_run[i] == -INFINITY ? l_run[i] : l_run[i] * ex2(x_run[i] - mx);  // (0, or NaN of NaN scores alone)
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
     l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-    // NaN scores alone leave the maximum at -inf: the row is not empty
-    if (m_run[i] == -INFINITY && l != 0.f) m_run[i] = 0.f;
     if (g == 0) {
       s_m[warp][2 * t + i] = m_run[i];
+      s_x[warp][2 * t + i] = mx;
       s_l[warp][2 * t + i] = l;
     }
   }
@@ -446,22 +475,26 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
         *reinterpret_cast<float4*>(dst + (8 * VB) * j + VB * g + 2 * m) =
             make_float4(o[j][m][i] * f, o[j][m][2 + i] * f, o[j][m + 1][i] * f, o[j][m + 1][2 + i] * f);
   }
-  // a row's statistics, by one warp's first lanes
+  // a row's last factor and the logarithm of its weight, by one warp's first lanes
   if (threadIdx.x < 8) {
     const int r = threadIdx.x;
-    float M = -INFINITY, l = 0.f;
+    float M = -INFINITY, X = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][r]);
+    for (int w = 0; w < kWarps; ++w) {
+      M = fmaxf(M, s_m[w][r]);
+      X = fmaxf(X, s_x[w][r]);
+    }
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) l += s_m[w][r] == -INFINITY ? 0.f : s_l[w][r] * ex2(s_m[w][r] - M);
-    s_row[r] = make_float2(M, l);
+    for (int w = 0; w < kWarps; ++w) l += s_x[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2(s_x[w][r] - X);
+    const float lw = X == -INFINITY ? l : X + __log2f(l);  // (without a maximum l is 0 or NaN)
+    s_row[r] = l == 0.f ? make_float2(0.f, -INFINITY) : make_float2(ex2(M - lw), lw);  // no visible key: zeros
   }
   __syncthreads();
   const bool whole = u0 == 0 && u1 == units;
 #pragma unroll
   for (int e = threadIdx.x; e < 8 * (D / 4); e += kWarps * 32) {
     const int r = e / (D / 4), c4 = e - r * (D / 4);
-    const float M = s_row[r].x, l = s_row[r].y;
+    const float f = s_row[r].x, lw = s_row[r].y;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -475,14 +508,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     if (whole) {
       if (row < rows) {
         const int qi = row / a.group, hl = row - qi * a.group;
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
         bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
-        *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
       }
     } else {
       const size_t pr = ((size_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * 8 + r;
-      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = acc;
-      if (c4 == 0) a.part_ml[pr] = make_float2(M, l);
+      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      if (c4 == 0) a.part_ml[pr] = part_weight(lw);
     }
   }
   unit += u1 - u0;

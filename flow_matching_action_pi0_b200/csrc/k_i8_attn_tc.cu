@@ -1,31 +1,37 @@
 // Attention over the int8 K/V cache, and fresh bf16 keys behind it, for many
 // query rows: the denoise loop's chunk of action tokens, or a causal prompt.
 //
-// Mathematics as in k_i8_attn.cu.  The query heads that share a KV head times
-// the queries (row = query * group + head-in-group, so that a tile spans few
-// queries and a causal tile skips the keys behind its last one) are cut into
-// tiles of 128 rows, the M dimension of tcgen05.mma.  Per chunk of 64 keys:
+// Mathematics as in k_i8_attn.cu: scores are products with the codes (bf16
+// integers here), and c = p vs, in units of the largest contribution, is
+// rounded to fp16 against V codes as fp16 integers.  Fresh tiles take c and V in
+// bf16, whose range fresh values may need.  The query heads that share a KV
+// head times the queries (row = query * group + head-in-group, so that a tile
+// spans few queries and a causal tile skips the keys behind its last one) are
+// cut into tiles of 128 rows, the M dimension of tcgen05.mma.  Per chunk of 64
+// keys:
 //   converters (8 warps)  read the codes (16-byte loads, the next chunk's in
 //                         flight while this one is written), turn them into
-//                         bf16 integers (exact) in the 128-byte swizzled tiles
-//                         the MMA reads; fresh keys and values are copied as
-//                         they are
+//                         integers (exact; K bf16, V fp16) in the 128-byte
+//                         swizzled tiles the MMA reads; fresh keys and values
+//                         are copied as they are
 //   two MMA warps         S = Q K^T (128 x 64, double-buffered in TMEM) and
 //                         O += P V (P read from TMEM, V read MN-major): an
 //                         issuing warp gets one instruction in thirty cycles
 //                         or so beside the others, and one warp for both was
 //                         part of the chunk-to-chunk chain
-//   scale warp            the chunk's key and value scales
-//   softmax (16 warps)    four threads per row: scores x key scale, online
-//                         softmax in the log2 domain (O is rescaled only when
-//                         the maximum grows by more than 2^8), P x value scale
-//                         as bf16 over S's own columns.  The chunk-to-chunk
-//                         chain runs through it, so its latency counts: with
-//                         two threads per row a chunk took 2900 cycles.
+//   scale warp            the chunk's key and value scales, see there
+//   softmax (16 warps)    four threads per row: online softmax in the log2
+//                         domain (O is rescaled only when the maximum grows by
+//                         more than 2^8), c over S's own columns.  The
+//                         chunk-to-chunk chain runs through it, so its latency
+//                         counts: with two threads per row a chunk took 2900
+//                         cycles.
 // Bound: the softmax and conversion work per tile, between the tensor cores'
 // and the cache's floors (K and V of a sequence are converted once per tile).
-// Key splits (small batches) write unnormalised fp32 rows with their maximum
-// and sum to the workspace; k_kv8_merge joins them.
+// Key splits (small batches) write fp32 averages with the logarithm of their
+// weight to the workspace; k_kv8_merge joins them.
+#include <cuda_fp16.h>
+
 #include "int8.h"
 #include "launch.cuh"
 
@@ -40,6 +46,7 @@ constexpr int kMmaWarp = kSmxWarps, kPvWarp = kMmaWarp + 1, kScaleWarp = kMmaWar
 constexpr int kConv = 128;                 // converter threads per operand
 constexpr int kThreads = kConvWarp * 32 + 2 * kConv;
 constexpr int KP = CK / 4;                 // keys per softmax part
+constexpr int kSc = 2 * CK + 4;            // a chunk's scales: ks [64], vs' or log2 vs [64], (narrow, E)
 constexpr long long kDrainNs = 4000000000LL;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -85,12 +92,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Two signed bytes in bits 0-7 and 16-23 -> bf16x2, exactly (see k_i8_attn.cu).
+// Two signed bytes in bits 0-7 and 16-23 of w (the other bits are ignored) ->
+// bf16x2, exactly: with v the low 7 bits and s the sign bit, 0x4300 | v is
+// 128 + v and 0x4300 | s << 7 is 128 (1 + s); their difference is v - 128 s.
 __device__ __forceinline__ uint32_t bytes_bf16x2(uint32_t w) {
   const uint32_t a = (w & 0x007F007Fu) | 0x43004300u;
   const uint32_t b = (w & 0x00800080u) | 0x43004300u;
   const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Bytes 0, 1 (sel 0x4140) or 2, 3 (0x4342) of codes ^ 0x80 -> fp16x2, exactly:
+// 0x6400 | u is 1024 + u, u = code + 128.
+__device__ __forceinline__ uint32_t biased_f16x2(uint32_t u, uint32_t sel) {
+  const uint32_t w = __byte_perm(u, 0x64646464u, sel);
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __floats2half2_rn(1152.f, 1152.f));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 // OR over the 128 threads of the four warps that share 32 rows.
@@ -169,7 +191,7 @@ template <int D>
 struct Smem {
   static constexpr uint32_t kTile = CK * D * 2;  // one chunk of K (or V) in bf16
   static constexpr uint32_t q = 0, k = QROWS * D * 2, v = k + 2 * kTile, sc = v + 2 * kTile;
-  static constexpr uint32_t pm = sc + 2 * 2 * CK * 4;    // scales: 2 chunks of [ks 64 | vs 64]
+  static constexpr uint32_t pm = sc + 2 * kSc * 4;
   static constexpr uint32_t l = pm + 4 * QROWS * 4;      // partial maxima [4][128]
   static constexpr uint32_t bar = l + 4 * QROWS * 4;     // partial sums [4][128]
   static constexpr uint32_t total = bar + 256 + 1024;
@@ -289,7 +311,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         break;
       }
       const uint32_t dst = dst0 + (uint32_t)slot * L::kTile;
-      if (c < nc) {
+      if (c < nc && is_v) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const uint32_t at = dst + u * 8 * 128;
+          const uint32_t w[4] = {raw[u].x ^ 0x80808080u, raw[u].y ^ 0x80808080u, raw[u].z ^ 0x80808080u, raw[u].w ^ 0x80808080u};
+          uint32_t o[8];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            o[2 * q] = biased_f16x2(w[q], 0x4140);
+            o[2 * q + 1] = biased_f16x2(w[q], 0x4342);
+          }
+          sts128(at + sw0, o[0], o[1], o[2], o[3]);
+          sts128(at + sw1, o[4], o[5], o[6], o[7]);
+        }
+      } else if (c < nc) {
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
           const uint32_t at = dst + u * 8 * 128;
@@ -328,6 +364,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     // lane l: key and value scales of keys l and l + 32, the next chunk's in
     // flight; a slot is written again only after its chunk's PV
     const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
+    //
+    // A chunk whose value scales lie within a factor 64 of one another takes the
+    // smallest one's exponent E for all: c = exp2(s ks + E - ref) vs', vs' =
+    // vs / 2^E in [1, 128) (c stays below 2^15), and the exponentials serve the
+    // row sums too.  Others take log2 vs
+    // key by key, so that a large row that a query does not see or weigh, or a
+    // zero one that it weighs most, costs the others nothing.
     float k[2], v[2];
     auto load = [&](int c) {
 #pragma unroll
@@ -335,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         const int at = lane + 32 * j;
         const bool in = c < nc ? c * CK + at < seen : (c - nc) * CK + at < a.n_new;
         k[j] = !in ? 0.f : c < nc ? __ldg(a.c.k_scale + base + c * CK + at) * a.scale_log2 : a.scale_log2;
-        v[j] = !in ? 0.f : c < nc ? __ldg(a.c.v_scale + base + c * CK + at) : 1.f;
+        v[j] = !in ? -0.f : c < nc ? __ldg(a.c.v_scale + base + c * CK + at) : 1.f;
       }
     };
     if (nch > 0) load(c0);
@@ -346,11 +389,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         set_error(a.err, DEV_TIMEOUT);
         break;
       }
+      // exponents of the largest and the smallest scale (bits of non-negative
+      // floats sort as integers; NaN above all, -0 marks a place without a key)
+      const uint32_t b0 = __float_as_uint(v[0]), b1 = __float_as_uint(v[1]);
+      const int hi = (int)(__reduce_max_sync(0xffffffffu, max(b0 & 0x7FFFFFFFu, b1 & 0x7FFFFFFFu)) >> 23);
+      const int lo = (int)(__reduce_min_sync(0xffffffffu, min(b0, b1)) >> 23);
+      const bool narrow = hi < 255 && lo > 0 && hi - lo <= 6;
+      const int e = narrow ? lo - 127 : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-E (-120 <= E <= 121)
+      float* sl = s_sc + slot * kSc;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        s_sc[slot * 2 * CK + lane + 32 * j] = k[j];
-        s_sc[slot * 2 * CK + CK + lane + 32 * j] = v[j];
+        const int at = lane + 32 * j;
+        sl[at] = k[j];
+        sl[CK + at] = narrow ? v[j] * down : __log2f(v[j]);  // (0, with codes 0: -inf)
       }
+      if (lane == 0) *reinterpret_cast<float2*>(sl + 2 * CK) = make_float2(narrow ? 1.f : 0.f, (float)e);
       mbar_arrive(&sc_full[slot]);
       if (i + 1 < nch) load(c0 + i + 1);
     }
@@ -388,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
           __syncwarp();
         }
       } else {
-        constexpr uint32_t idesc_o = idesc_bf16(QROWS, D, 0, 1);
+        constexpr uint32_t idesc_new = idesc_bf16(QROWS, D, 0, 1);
+        constexpr uint32_t idesc_old = idesc_new & ~((7u << 7) | (7u << 10));  // A and B fp16 (format 0)
         const uint64_t v_desc = sw128_desc(smem_u32(smem + L::v), CK * 128, 1024);
         const uint32_t v_lo = (uint32_t)v_desc, hi = (uint32_t)(v_desc >> 32);
         for (int i = 0; good && i < nch; ++i) {
@@ -396,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
           good = mbar_wait(&v_full[st], (i >> 1) & 1, a.err.wait_ns) && mbar_wait(&p_full[st], (i >> 1) & 1, a.err.wait_ns);
           if (!(good = __all_sync(0xffffffffu, good))) break;
           tc_fence_after();
+          const uint32_t idesc_o = c0 + i < nc ? idesc_old : idesc_new;
           const uint32_t p = tmem + (uint32_t)(st * CK), vl = v_lo + (uint32_t)st * (L::kTile >> 4);
           if (elect_one()) {
             mma_ts(t_o, p, vl, hi, idesc_o, i > 0 ? 1u : 0u);
@@ -449,8 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     const int rq = qt * QROWS + r;
     const int oc0 = part * (D / 4);
     const int lim = a.causal ? min(len, len - a.n_q + 1 + min(rq, rows - 1) / a.group) : len;
-    float ref = 0.f, l_run = 0.f;  // reference in the log2 domain; has: some key was visible
-    bool ok = true, has = false;
+    float ref = 0.f;               // reference of c, the row's, in the log2 domain; has: some key was visible
+    float xref = 0.f, l_run = 0.f; // the sum's, this part's of the row (k_i8_attn.cu says why they differ)
+    bool ok = true, has = false, xhas = false;
     for (int i = 0; i < nch; ++i) {
       const int st = i & 1, c = c0 + i;
       const bool got = mbar_wait(&sc_full[st], (i >> 1) & 1, a.err.wait_ns) &&
@@ -461,15 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       tmem_ld16(tmem + (uint32_t)(st * CK) + lane_off + part * KP, sv);
       tmem_ld_wait();
       reg_fence16(sv);
-      const float* sc = s_sc + st * 2 * CK + part * KP;
+      const float* sc = s_sc + st * kSc + part * KP;
+      const float2 ch = *reinterpret_cast<const float2*>(s_sc + st * kSc + 2 * CK);
+      const bool narrow = ch.x != 0.f;
       // visible keys of this part's
       const int vis = (c < nc ? lim - c * CK : a.n_new - (c - nc) * CK) - part * KP;
-      // Scores in units of the row's reference: y = s ks - ref.  The reference
-      // (a running maximum) moves only when a score exceeds it by more than 8, a
-      // factor 256, so that O is rescaled rarely; until then no part needs
-      // another part's maximum, only everyone's word that it stays.
+      // Exponents in units of the row's reference: y = s ks + E - ref.  The reference
+      // (a running maximum) moves only when an exponent of c exceeds it by more
+      // than 8, a factor 256, so that O is rescaled rarely; until then no part
+      // needs another part's maximum, only everyone's word that it stays.
       float2* s2 = reinterpret_cast<float2*>(sv);
-      const float2 nref = make_float2(-ref, -ref);
+      const float2 nref = make_float2(ch.y - ref, ch.y - ref);
 #pragma unroll
       for (int j = 0; j < KP / 2; j += 2) {
         const float4 k4 = *reinterpret_cast<const float4*>(sc + 2 * j);
@@ -483,7 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       float mt[KP / 4];
 #pragma unroll
       for (int j = 0; j < KP / 4; ++j) mt[j] = fmaxf(max3(sv[4 * j], sv[4 * j + 1], sv[4 * j + 2]), sv[4 * j + 3]);
-      const float pmax = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]);
+      float xmax = fmaxf(max3(mt[0], mt[1], mt[2]), mt[3]), pmax = xmax;
+      if (!narrow) {
+        pmax = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < KP; ++j) pmax = fmaxf(pmax, j < vis ? sv[j] + sc[CK + j] : -INFINITY);
+      }
       // Every part of the rows has its scores in registers (P overwrites S).
       // A part that must stop asks for a move too, so all meet below.
       const bool mine = got && s_flag[0] == 0;
@@ -499,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         const bool move = has ? cmax > 8.f : cmax != -INFINITY;  // (NaN alone: the reference stays)
         const float up = move && cmax == cmax ? cmax : 0.f;
         ref += up;
+        xmax -= up;
         alpha = has ? ex2(-up) : 1.f;
         has = has || move;
         const float2 nup = make_float2(-up, -up);
@@ -506,29 +571,57 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         for (int j = 0; j < KP / 2; ++j) s2[j] = add2(s2[j], nup);
         rows_and(1 + (warp & 3), true);  // the maxima are read: the next move may write them
       }
-      float2 sum[2];
-#pragma unroll
-      for (int j = 0; j < KP / 2; ++j) {
-        s2[j].x = ex2(s2[j].x);
-        s2[j].y = ex2(s2[j].y);
-        sum[j & 1] = j < 2 ? s2[j] : add2(sum[j & 1], s2[j]);
+      // The sum: 2^(y + f) in units of its own reference, which moves when a
+      // score exceeds it by 64 (fp32 holds both sides).
+      float f = ref - ch.y - xref;
+      const bool far = xmax > -INFINITY && (!xhas || xmax + f > 64.f);
+      if (__any_sync(0xffffffffu, far)) {
+        if (far) {
+          if (xhas) l_run *= ex2(-(xmax + f));
+          xref += xmax + f;
+          f = -xmax;
+          xhas = true;
+        }
       }
-      sum[0] = add2(sum[0], sum[1]);
-      l_run = l_run * alpha + (sum[0].x + sum[0].y);
+      // A narrow chunk's exponentials serve both sums, but for rows to which the
+      // chunk's largest contribution is next to nothing, though its weight may not be.
+      const bool shared = narrow && !__any_sync(0xffffffffu, xmax < -60.f && xmax > -INFINITY);
+      if (!shared) {
+#pragma unroll
+        for (int j = 0; j < KP; ++j) l_run += ex2(sv[j] + f);
+      }
+      if (narrow) {
+#pragma unroll
+        for (int j = 0; j < KP / 2; ++j) {
+          s2[j].x = ex2(s2[j].x);
+          s2[j].y = ex2(s2[j].y);
+        }
+        if (shared) {
+          float2 sum[2] = {s2[0], s2[1]};
+#pragma unroll
+          for (int j = 2; j < KP / 2; ++j) sum[j & 1] = add2(sum[j & 1], s2[j]);
+          sum[0] = add2(sum[0], sum[1]);
+          l_run += (sum[0].x + sum[0].y) * ex2(fminf(f, 126.f));  // (f <= 124 unless the part sees no key)
+        }
+#pragma unroll
+        for (int j = 0; j < KP / 2; j += 2) {
+          const float4 v4 = *reinterpret_cast<const float4*>(sc + CK + 2 * j);
+          s2[j] = mul2(s2[j], make_float2(v4.x, v4.y));
+          s2[j + 1] = mul2(s2[j + 1], make_float2(v4.z, v4.w));
+        }
+      } else {  // masked places stay 0 whatever their scale is
+#pragma unroll
+        for (int j = 0; j < KP; ++j) sv[j] = j < vis ? ex2(sv[j] + sc[CK + j]) : 0.f;
+      }
       const bool scale_o = i > 0 && alpha != 1.f;
-#pragma unroll
-      for (int j = 0; j < KP / 2; j += 2) {
-        const float4 v4 = *reinterpret_cast<const float4*>(sc + CK + 2 * j);
-        s2[j] = mul2(s2[j], make_float2(v4.x, v4.y));
-        s2[j + 1] = mul2(s2[j + 1], make_float2(v4.z, v4.w));
-      }
-      if (vis < KP) {  // masked places stay 0 whatever their scale is
-#pragma unroll
-        for (int j = 0; j < KP; ++j) sv[j] = j < vis ? sv[j] : 0.f;
-      }
       uint32_t pk[KP / 2];
+      if (c < nc) {
 #pragma unroll
-      for (int j = 0; j < KP / 2; ++j) pk[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
+        for (int j = 0; j < KP / 2; ++j) pk[j] = pack_f16(sv[2 * j], sv[2 * j + 1]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < KP / 2; ++j) pk[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
+      }
       tmem_st8u(tmem + (uint32_t)(st * CK) + lane_off + part * (KP / 2), pk);
       if (__any_sync(0xffffffffu, scale_o)) {
         // O may be rescaled only once PV of the previous chunk has landed in it
@@ -557,17 +650,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     // PVs complete in issue order: the last chunk's commit covers them all
     if (nch > 0 && ok) ok = mbar_wait(&o_done[(nch - 1) & 1], ((nch - 1) >> 1) & 1, kDrainNs);
     s_l[part * QROWS + r] = l_run;
+    s_pm[part * QROWS + r] = xhas ? xref : -INFINITY;
     ok = rows_and(1 + (warp & 3), ok && s_flag[0] == 0);
     tc_fence_after();
-    const float l = ((s_l[r] + s_l[QROWS + r]) + s_l[2 * QROWS + r]) + s_l[3 * QROWS + r];
+    // the parts' sums in units of their largest reference X; a part without one
+    // has 0, or NaN of NaN scores alone
+    const float X = fmaxf(fmaxf(s_pm[r], s_pm[QROWS + r]), fmaxf(s_pm[2 * QROWS + r], s_pm[3 * QROWS + r]));
+    float l = 0.f;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const float x = s_pm[p * QROWS + r];
+      l += x == -INFINITY ? s_l[p * QROWS + r] : s_l[p * QROWS + r] * ex2(x - X);
+    }
+    const float lw = X == -INFINITY ? l : X + __log2f(l);
+    // O in units of 2^ref -> the average over the keys; no visible key: zeros
+    const float inv = l == 0.f ? 0.f : ex2(ref - lw);
     // Output rows go through shared memory (every MMA is done: the tiles are
     // free), so that a row leaves as one run of 16-byte stores; straight from
     // the registers, a warp's store touches 32 rows and the 128 rows of a tile
     // took 7000 cycles.  Chunks of 16 bytes are swizzled by the row.
-    const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible key: zeros
-    const bool some = ok && nch > 0 && l != 0.f;  // (NaN counts)
     const size_t pr0 = ((size_t)bg * splits + split) * ((size_t)gridDim.x * QROWS) + qt * QROWS;
-    if (splits > 1 && part == 0) a.part_ml[pr0 + r] = some ? make_float2(ref, l) : make_float2(-INFINITY, 0.f);
+    if (splits > 1 && part == 0) a.part_ml[pr0 + r] = part_weight(ok && l != 0.f ? lw : -INFINITY);
     const uint32_t stage = smem_u32(smem);
     const int esz = splits == 1 ? 2 : 4;
     const uint32_t rowb = (uint32_t)(D * esz), srow = stage + (uint32_t)r * rowb;
@@ -593,8 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
         const uint32_t ch = (uint32_t)(oc0 + j) / 4;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          sts128(srow + (((ch + t) ^ (r & 7)) << 4), __float_as_uint(ov[4 * t]), __float_as_uint(ov[4 * t + 1]),
-                 __float_as_uint(ov[4 * t + 2]), __float_as_uint(ov[4 * t + 3]));
+          sts128(srow + (((ch + t) ^ (r & 7)) << 4), __float_as_uint(ov[4 * t] * inv), __float_as_uint(ov[4 * t + 1] * inv),
+                 __float_as_uint(ov[4 * t + 2] * inv), __float_as_uint(ov[4 * t + 3] * inv));
       }
     }
     ok = rows_and(1 + (warp & 3), ok);

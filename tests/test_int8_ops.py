@@ -55,11 +55,12 @@ def attention_ref(q, k, v, lens, causal, k_new, v_new, scale):
     return o, a
 
 
-def assert_attention(got, o, a):
-    """P (times the value scale) is rounded to bf16 once, the output once; the
-    scores' fp32 sums (|q k| adds to some tens over d <= 256 terms) and the
-    2^-22 of exp2 move a probability by less than 2^-10."""
-    tol = a * (2.0 ** -8 + 2.0 ** -10) + o.abs() * 2.0 ** -8
+def assert_attention(got, o, a, more=0.0):
+    """A probability (times the value scale) is rounded once, to fp16 or bf16,
+    the output once; the scores' fp32 sums (|q k| adds to some tens over d <=
+    256 terms), 16-bit query digits and the 2^-22 of exp2 move a probability by
+    less than 2^-10."""
+    tol = a * (2.0 ** -8 + 2.0 ** -10) + o.abs() * 2.0 ** -8 + more
     over = ((got.cpu().double() - o).abs() - tol).max()
     assert over <= 0, f"beyond the bound by {over:.3e}"
 
@@ -393,6 +394,65 @@ def test_kv8_attention_causal_masks_nan_rows(nq, group):
         assert bool(torch.isnan(got[:, 2:]).all())
         assert torch.equal(got[:, :2], clean[:, :2])
         t[0, 0, at] = keep
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq,fresh,causal", [(1, 0, False), (4, 0, True), (40, 0, False), (40, 33, False), (60, 0, True)])
+def test_kv8_attention_rows_of_very_different_size(nq, fresh, causal):
+    """Value rows from 2^-60 to 2^60 side by side (a row's weight decides, not
+    its neighbours' size), zero rows, and huge rows where a query may not look."""
+    g = torch.Generator().manual_seed(nq + fresh)
+    B, cap, d, group = 2, 400, 128, 4
+    c = fm.KvCacheInt8(B, 1, cap, d)
+    k = torch.randn(B * cap, 1, d, generator=g)
+    size = torch.exp2(torch.randint(-60, 61, (B * cap, 1, 1), generator=g).float())
+    size[torch.rand(B * cap, 1, 1, generator=g) < 0.1] = 0.0
+    v = torch.randn(B * cap, 1, d, generator=g) * size
+    v[cap:] = torch.randn(cap, 1, d, generator=g)   # the second sequence: unit rows,
+    lens = [cap, 300]
+    v[cap + 300 - 3:cap + 300] *= 1e30               # huge ones at its last positions
+    c.write(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), torch.tensor([0, cap, 2 * cap], dtype=torch.int32, device="cuda"))
+    vals = [(t.double() * s.double().unsqueeze(-1)).cpu() for t, s in ((c.k, c.k_scale), (c.v, c.v_scale))]
+    q = torch.randn(B, nq, group, d, generator=g).to(torch.bfloat16)
+    new = [torch.randn(B, fresh, 1, d, generator=g).to(torch.bfloat16) for _ in range(2)] if fresh else [None, None]
+    o, a = attention_ref(q.double(), *vals, lens, causal, *[None if t is None else t.double() for t in new], d ** -0.5)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = c.attend(q.cuda(), n, causal=causal, k_new=None if not fresh else new[0].cuda(), v_new=None if not fresh else new[1].cuda())
+    # fp16 holds c = p vs / 2^ref in steps of 2^-24 at the bottom, an error of 2^-25
+    # at most, against a largest c of 1 at least; a channel adds cap + fresh of
+    # them, times codes up to 127.  In units of the output that is (cap + fresh)
+    # 2^-25 (127 max p vs), and 127 p vs is the largest |p v| of a key's channels,
+    # which is not above the row's largest a.
+    assert_attention(got, o, a, (cap + fresh) * 2.0 ** -25 * a.amax(-1, keepdim=True))
+    if causal:  # the queries before the huge rows see unit rows alone
+        assert float(got[1, :nq - 3].abs().max()) < 10
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq,fresh", [(1, 0), (4, 0), (40, 0), (40, 33)])
+def test_kv8_attention_weight_on_empty_values(nq, fresh):
+    """A key that takes nearly all the weight and has no value, or values of
+    2^-90: what the others contribute keeps its precision."""
+    g = torch.Generator().manual_seed(nq + fresh)
+    B, cap, d, group = 2, 300, 64, 4
+    c = fm.KvCacheInt8(B, 1, cap, d)
+    k = torch.randn(B * cap, 1, d, generator=g)
+    v = torch.randn(B * cap, 1, d, generator=g)
+    q = torch.randn(B, nq, group, d, generator=g)
+    q[..., 0] = 8.0
+    for b in range(B):
+        for at in (5, 130):  # score about 8 * 20 / 8 = 20 above the others'
+            k[b * cap + at] = 0.0
+            k[b * cap + at, 0, 0] = 20.0
+            v[b * cap + at] *= 0.0 if b == 0 else 2.0 ** -90
+    c.write(k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda(), torch.tensor([0, cap, 2 * cap], dtype=torch.int32, device="cuda"))
+    vals = [(t.double() * s.double().unsqueeze(-1)).cpu() for t, s in ((c.k, c.k_scale), (c.v, c.v_scale))]
+    q = q.to(torch.bfloat16)
+    new = [torch.randn(B, fresh, 1, d, generator=g).to(torch.bfloat16) for _ in range(2)] if fresh else [None, None]
+    o, a = attention_ref(q.double(), *vals, [cap] * B, False, *[None if t is None else t.double() for t in new], d ** -0.5)
+    n = torch.full((B,), cap, dtype=torch.int32, device="cuda")
+    got = c.attend(q.cuda(), n, k_new=None if not fresh else new[0].cuda(), v_new=None if not fresh else new[1].cuda())
+    assert_attention(got, o, a)
 
 
 @pytest.mark.gpu
