@@ -219,6 +219,7 @@ pae_status pae_quantize_rows(const void* x, long long ldx, int rows, int width, 
   const char* fn = "pae_quantize_rows";
   if (!known(dtype)) return fail(PAE_ERR_ARG, "%s: dtype must be PAE_FP32 or PAE_BF16", fn);
   if (rows < 0 || width < 1) return fail(PAE_ERR_ARG, "%s: rows must be >= 0 and width >= 1", fn);
+  if (rows > kMaxCapacity || width > kMaxCapacity) return fail(PAE_ERR_UNSUPPORTED, "%s: rows and width must be at most 2^30", fn);
   if (!(rms_eps >= 0.f) || std::isinf(rms_eps)) return fail(PAE_ERR_ARG, "%s: rms_eps must be 0 (no norm) or a finite positive number", fn);
   if (rows == 0) return PAE_OK;
   if (!x || !codes || !scale) return fail(PAE_ERR_ARG, "%s: a pointer argument is NULL", fn);

@@ -75,6 +75,9 @@ def _dtype_code(dtype: torch.dtype, what: str) -> int:
     return code
 
 
+_MOST = 1 << 30  # of a size: the library takes 32-bit integers
+
+
 def _check_vector(t: torch.Tensor, n: int, dtype: torch.dtype, what: str) -> None:
     if t.dtype != dtype or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n}")
@@ -89,11 +92,13 @@ def quantize_rows(x: torch.Tensor, rms_eps: Optional[float] = None) -> Tuple[tor
     rows, width = x.shape
     if width < 1:
         raise ValueError("x must have width >= 1")
+    if rows > _MOST or width > _MOST:
+        raise ValueError("x must have at most 2^30 rows and columns")
     ldx, unit = x.stride()
     if unit != 1 and width > 1:
         raise ValueError("x must be contiguous along width")
     code = _dtype_code(x.dtype, "x")
-    if rms_eps is not None and not rms_eps > 0:
+    if rms_eps is not None and not rms_eps > 1e-45:  # (the library takes a float, 0 stands for no norm)
         raise ValueError("rms_eps must be positive")
     device = _check_device(x)
     codes = x.new_empty((rows, width), dtype=_int8)
@@ -113,6 +118,8 @@ def linear_i8(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     n, kw = w.shape
     if k != kw:
         raise ValueError("x [tokens, k] and w [n, k] must share k")
+    if tokens > _MOST or n > _MOST or k > _MOST:
+        raise ValueError("tokens, n and k must be at most 2^30")
     if x.dtype != _int8 or w.dtype != _int8:
         raise ValueError("x and w must be int8 codes")
     if not (x.is_contiguous() and w.is_contiguous()):
@@ -164,6 +171,8 @@ class KvCacheInt8:
         cu = at = None
         if cu_rows is not None:
             n_seq = cu_rows.shape[0] - 1
+            if n_seq > self.shape[0]:
+                raise ValueError(f"cu_rows names {n_seq} sequences, the cache has {self.shape[0]} slots")
             _check_vector(cu_rows, n_seq + 1, _int32, "cu_rows")
             cu = cu_rows.data_ptr()
         if start is not None:
@@ -185,6 +194,8 @@ class KvCacheInt8:
         Rows outside every sequence or past the capacity are dropped."""
         if k.shape != v.shape or k.dtype != v.dtype:
             raise ValueError("k and v must have the same shape and type")
+        if k.dim() != 3 or k.shape[0] > _MOST:
+            raise ValueError("k and v must be [rows, n_kv_heads, head_dim] with at most 2^30 rows")
         code = _dtype_code(k.dtype, "k and v")
         ks, vs = self._strides(k, "k"), self._strides(v, "v")
         n_seq, cu, at = self._seqs(cu_rows, start)
@@ -196,6 +207,8 @@ class KvCacheInt8:
              dtype: torch.dtype = torch.bfloat16) -> Tuple[torch.Tensor, torch.Tensor]:
         """The rows that write places for the same arguments, as the values
         their codes stand for; rows without a place are zeros."""
+        if not 0 <= n_rows <= _MOST:
+            raise ValueError("n_rows must be in [0, 2^30]")
         code = _dtype_code(dtype, "dtype")
         n_seq, cu, at = self._seqs(cu_rows, start)
         device = _check_device(self.k, cu_rows, start)
@@ -243,6 +256,8 @@ class KvCacheInt8:
             if k_new.shape != v_new.shape or k_new.shape[0] != n_seq:
                 raise ValueError("k_new and v_new must be [n_seq, n_new, n_kv_heads, head_dim]")
             n_new, kp, vp = k_new.shape[1], k_new.data_ptr(), v_new.data_ptr()
+            if n_new > _MOST:
+                raise ValueError("k_new and v_new must have at most 2^30 rows")
             ks, vs = self._rows(k_new, hk, "k_new"), self._rows(v_new, hk, "v_new")
         if out is None:
             out = q.new_empty(q.shape)

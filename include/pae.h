@@ -379,20 +379,23 @@ void pae_int8_clear_error(void);
  * codes [rows][width] and scale [rows].  rms_eps > 0 quantises the RMSNorm of
  * each row, x / sqrt(mean(x^2) + rms_eps) (no gain: fold one into the weights
  * that follow); 0 quantises x itself.  Also lays out weights for
- * pae_linear_i8, once: rows = output channels. */
+ * pae_linear_i8, once: rows = output channels.  rows and width at most 2^30
+ * (else PAE_ERR_UNSUPPORTED); rows == 0 is a no-op. */
 pae_status pae_quantize_rows(const void* x, long long ldx, int rows, int width, int dtype, float rms_eps,
                              signed char* codes, float* scale, pae_stream stream);
 
 /* y[t][f] = (sum_k x[t][k] w[f][k]) x_scale[t] w_scale[f]: x [tokens][k], w
  * [n][k] 8-bit codes (16-byte aligned), exact 32-bit sums, y [tokens][n] with
  * row stride ldy >= n in PAE_FP32 or PAE_BF16 (rounded once).  k a multiple of
- * 16, at most 131056 (else PAE_ERR_UNSUPPORTED); tokens == 0 is a no-op. */
+ * 16, at most 131056, tokens and n at most 2^24 (else PAE_ERR_UNSUPPORTED);
+ * tokens == 0 is a no-op. */
 pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signed char* w, const float* w_scale,
                          int tokens, int n, int k, void* y, long long ldy, int dtype, pae_stream stream);
 
 /* An int8 K/V cache in buffers of the caller: codes [n_slots][n_kv_heads]
  * [capacity][head_dim] (16-byte aligned), one fp32 scale per (slot, head,
- * position).  head_dim 64, 128 or 256. */
+ * position).  head_dim 64, 128 or 256, n_kv_heads at most 65535 (else
+ * PAE_ERR_UNSUPPORTED), capacity at most 2^30. */
 typedef struct {
   signed char *k, *v;
   float *k_scale, *v_scale;
@@ -408,7 +411,7 @@ typedef struct {
  * rows must start on 16 bytes, so K and V may be slices of one projection).
  * Write leaves every position that no row goes to as it was; rows outside the
  * sequences or past the capacity are dropped.  Read fills such rows with
- * zeros. */
+ * zeros.  n_rows at most 2^30 (else PAE_ERR_UNSUPPORTED). */
 pae_status pae_kv8_write(const pae_kv8* cache, const void* k, const void* v, const long long* k_strides,
                          const long long* v_strides, const int* cu_rows, const int* start, int n_seq, int n_rows,
                          int dtype, pae_stream stream);
@@ -429,7 +432,12 @@ pae_status pae_kv8_read(const pae_kv8* cache, void* k, void* v, const long long*
  * elements, multiples of 8, on 16 bytes.  out may equal q.  workspace:
  * pae_kv8_workspace bytes (the same sizes; 0 possible), not shared by calls
  * that may overlap; its contents carry nothing from call to call.
- * PAE_ERR_UNSUPPORTED: n_seq * n_kv_heads > 65535. */
+ * PAE_ERR_UNSUPPORTED: n_seq * n_kv_heads > 65535, n_q times the query heads
+ * of a KV head > 2^22.
+ * Precision: scores are fp32; a probability times its value's scale is rounded
+ * to fp16 in units of the row's largest one (cached keys; what is below 2^-25
+ * of it, far less than one of its own code steps, is lost) or to bf16 (fresh
+ * keys), sums are fp32. */
 typedef struct {
   const int* lens;
   const void* q;

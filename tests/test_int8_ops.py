@@ -6,6 +6,7 @@ A rounding to a type t is off by at most eps(t) / 2 relative to the value
 """
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -101,6 +102,8 @@ def test_quantize_rows_refusals(lib):
     for kw in (dict(x=None), dict(codes=None), dict(scale=None), dict(ldx=63), dict(rows=-1), dict(width=0),
                dict(dtype=fm.PAE_W4A16), dict(eps=-1.0), dict(eps=math.nan), dict(eps=math.inf), dict(x=P16 + 1)):
         assert call(**kw) == fm.PAE_ERR_ARG, kw
+    assert call(rows=(1 << 30) + 1) == fm.PAE_ERR_UNSUPPORTED
+    assert call(width=(1 << 30) + 1, ldx=1 << 31) == fm.PAE_ERR_UNSUPPORTED
     assert call(rows=0, x=None) == fm.PAE_OK
 
 
@@ -174,6 +177,32 @@ def test_wrappers_refuse_cpu_tensors_and_bad_shapes():
         fm.linear_i8(x.to(torch.int8), torch.ones(2), x.to(torch.int8), torch.ones(2))
     with pytest.raises(ValueError):
         fm.linear_i8(x.to(torch.int8), torch.ones(2), torch.zeros(4, 16, dtype=torch.int8), torch.ones(4))
+    # sizes that do not fit the library's integers (views of one element)
+    huge = torch.zeros(1, 1).expand((1 << 32) + 2, 1)
+    with pytest.raises(ValueError, match="2\\^30"):
+        fm.quantize_rows(huge)
+    with pytest.raises(ValueError, match="2\\^30"):
+        fm.quantize_rows(huge.t())
+    codes = torch.zeros(1, 1, dtype=torch.int8).expand((1 << 32) + 2, 16)
+    with pytest.raises(ValueError, match="2\\^30"):
+        fm.linear_i8(codes, torch.ones(1), codes[:4], torch.ones(4))
+    with pytest.raises(ValueError):
+        fm.quantize_rows(x, 1e-60)  # 0 as a float
+
+
+@pytest.mark.gpu
+def test_cache_refuses_sizes_past_its_integers():
+    c = fm.KvCacheInt8(2, 1, 64, 64)
+    row = torch.zeros(1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="2\\^30"):
+        c.write(row.expand((1 << 32) + 2, 1, 64), row.expand((1 << 32) + 2, 1, 64))
+    with pytest.raises(ValueError, match="2\\^30"):
+        c.read(None, None, (1 << 32) + 2)
+    with pytest.raises(ValueError, match="slots"):
+        c.write(row, row, torch.zeros(4, dtype=torch.int32, device="cuda"))
+    many = row[None].expand(2, (1 << 32) + 2, 1, 64)
+    with pytest.raises(ValueError, match="2\\^30"):
+        c.attend(row[None].expand(2, 1, 1, 64), torch.zeros(2, dtype=torch.int32, device="cuda"), k_new=many, v_new=many)
 
 
 # -------------------------------------------------------------- row quantiser
@@ -586,3 +615,42 @@ def test_two_streams_with_their_own_plans():
     torch.cuda.synchronize()
     for w, o in zip(want, outs):
         assert torch.equal(w, o)
+
+
+CAPTURE_FIRST = """
+import torch
+import flow_matching_action_pi0_b200 as fm
+torch.cuda.set_device(0)
+fm.pae_int8_init()
+x = torch.linspace(-1, 1, 70 * 128, device="cuda").view(70, 128).bfloat16()
+w, ws = torch.ones(256, 128, dtype=torch.int8, device="cuda"), torch.ones(256, device="cuda")
+cache = fm.KvCacheInt8(1, 1, 100, 128)
+n = torch.tensor([70], dtype=torch.int32, device="cuda")
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    q, s = fm.quantize_rows(x, 1e-6)
+    y = fm.linear_i8(q, s, w, ws)
+    cache.write(y[:, None, :128], y[:, None, 128:])
+    one, many = cache.attend(x[None, :1, None], n), cache.attend(x[None, :, None], n)
+    back = cache.read(None, None, 70)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (q, s, y, one, many, *back)]
+q, s = fm.quantize_rows(x, 1e-6)
+y = fm.linear_i8(q, s, w, ws)
+cache.write(y[:, None, :128], y[:, None, 128:])
+want = [q, s, y, cache.attend(x[None, :1, None], n), cache.attend(x[None, :, None], n), *cache.read(None, None, 70)]
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+fm.pae_int8_sync()
+print("captured")
+"""
+
+
+@pytest.mark.gpu
+def test_a_capture_may_hold_the_first_calls():
+    """After pae_int8_init every operator may run for the first time inside a capture."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
