@@ -1,4 +1,5 @@
-"""Build libpae.so (the C-ABI library of include/pae.h) in-tree for sm_100a.
+"""Build libpae.so (the C-ABI library of include/pae.h) in-tree for sm_100a, and
+_int8_tensors.so, the tensor side of int8.py, against the installed PyTorch.
 
     python -m flow_matching_action_pi0_b200.build [--force] [--verbose]
 
@@ -14,12 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libpae.so")
+TENSORS = os.path.join(HERE, "_int8_tensors.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -34,11 +37,27 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+_TENSORS_SRC = os.path.join(CSRC, "int8_tensors.cpp")
+
+
+def _tensors_command():
+    import torch
+    from torch.utils import cpp_extension as ext
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("no C++ compiler found")
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+            *(f"-isystem{p}" for p in (*ext.include_paths("cuda"), sysconfig.get_paths()["include"])),
+            _TENSORS_SRC, "-o", TENSORS + ".tmp", *(f"-L{p}" for p in ext.library_paths("cuda")),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TENSORS):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TENSORS))
+    deps = sources() + [_TENSORS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -46,6 +65,7 @@ def _stale() -> bool:
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     if not force and not _stale():
         return LIB
+    tensors = subprocess.Popen(_tensors_command(), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     flags = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -68,14 +88,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             sys.stdout.write(out)
         if p.returncode:
             failed.append(src)
+    out, _ = tensors.communicate()
+    if tensors.returncode:
+        sys.stdout.write(out)
+        failed.append(_TENSORS_SRC)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs + ["-lcudart_static", "-ldl",
                                                                                       "-lpthread", "-lrt"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
+    os.replace(TENSORS + ".tmp", TENSORS)
     os.replace(tmp, LIB)
     return LIB
 

@@ -190,6 +190,61 @@ def test_wrappers_refuse_cpu_tensors_and_bad_shapes():
         fm.quantize_rows(x, 1e-60)  # 0 as a float
 
 
+def test_a_cache_in_host_memory_is_refused():
+    c = fm.KvCacheInt8(1, 1, 8, 64, device="cpu")
+    row = torch.zeros(1, 1, 64, dtype=torch.bfloat16)
+    n = torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: c.write(row, row), lambda: c.read(None, None, 1), lambda: c.attend(row[None], n),
+                 lambda: c.write(row, row, start=n)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+
+
+@pytest.mark.gpu
+def test_wrappers_refuse_what_does_not_fit():
+    """Wrong types, shapes, layouts, devices and plans, each named by its error
+    and leaving the operators usable."""
+    bf = dict(device="cuda", dtype=torch.bfloat16)
+    x, w = torch.ones(4, 64, **bf), torch.ones(8, 64, device="cuda", dtype=torch.int8)
+    q, s = fm.quantize_rows(x)
+    ws = torch.ones(8, device="cuda")
+    c = fm.KvCacheInt8(2, 2, 64, 64)
+    rows = torch.ones(3, 2, 64, **bf)
+    n = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    qs, new = torch.ones(2, 20, 4, 64, **bf), torch.ones(2, 5, 2, 64, **bf)
+    plan = c.plan(2, 20, 4)
+    cu = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")
+    bad = [lambda: fm.quantize_rows(x.half()), lambda: fm.quantize_rows(x[0]), lambda: fm.quantize_rows(x.t()[:, :2]),
+           lambda: fm.quantize_rows(x[:, :0]), lambda: fm.quantize_rows(x, 0.0), lambda: fm.quantize_rows(x, -1.0),
+           lambda: fm.linear_i8(x, s, w, ws), lambda: fm.linear_i8(q, s[:3], w, ws), lambda: fm.linear_i8(q, s, w, ws.double()),
+           lambda: fm.linear_i8(q, s, w.t(), ws), lambda: fm.linear_i8(q.cpu(), s, w, ws), lambda: fm.linear_i8(q, s, w, ws, torch.float16),
+           lambda: fm.linear_i8(q, s, w, ws, out=torch.empty(4, 9, **bf)), lambda: fm.linear_i8(q, s, w, ws, out=torch.empty(8, 4, **bf).t()),
+           lambda: c.write(rows, rows[:2]), lambda: c.write(rows, rows.float()), lambda: c.write(rows[0], rows[0]),
+           lambda: c.write(rows[:, :1], rows[:, :1]), lambda: c.write(rows, rows, cu.long()), lambda: c.write(rows, rows, cu[:0]),
+           lambda: c.write(rows, rows, cu.cpu()), lambda: c.write(rows, rows, cu, n[:1]), lambda: c.read(cu, None, -1),
+           lambda: c.read(cu, None, 3, torch.float16), lambda: c.attend(qs[0], n), lambda: c.attend(qs.float(), n),
+           lambda: c.attend(qs, n[:1]), lambda: c.attend(qs, n.cpu()), lambda: c.attend(qs, n, scale=0.0),
+           lambda: c.attend(qs, n, k_new=new), lambda: c.attend(qs, n, k_new=new, v_new=new[:, :4]),
+           lambda: c.attend(qs, n, k_new=new[:1], v_new=new[:1]), lambda: c.attend(qs, n, out=qs[:, :1]),
+           lambda: c.attend(qs, n, out=qs.float()), lambda: c.attend(qs, n, k_new=new, v_new=new, plan=plan),
+           lambda: c.attend(qs[:, :, :, :32], n), lambda: c.attend(qs[:, :19], n, plan=plan)]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was accepted")
+    for call in (lambda: fm.quantize_rows([1.0]), lambda: fm.linear_i8(q, s, w, None), lambda: c.write(rows, None),
+                 lambda: fm.quantize_rows(x, "eps"), lambda: c.read(cu, None, "rows"), lambda: c.read(cu, None, 3, "bf16")):
+        with pytest.raises(TypeError):
+            call()
+    for call in (lambda: c.attend(qs, n, causal=True, k_new=new, v_new=new), lambda: c.attend(qs, n, scale=float("nan")),
+                 lambda: fm.linear_i8(q[:, :24].contiguous(), s, w[:, :24].contiguous(), ws)):
+        with pytest.raises(fm.PaeError):
+            call()
+    c.write(rows, rows, cu)
+    assert bool((c.attend(qs, torch.tensor([1, 2], dtype=torch.int32, device="cuda"), plan=plan) == 1).all())
+    fm.pae_int8_sync()
+
+
 @pytest.mark.gpu
 def test_cache_refuses_sizes_past_its_integers():
     c = fm.KvCacheInt8(2, 1, 64, 64)
