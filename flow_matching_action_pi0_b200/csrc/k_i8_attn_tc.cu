@@ -187,6 +187,27 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
+// Query and head-in-group of the rows r, r + step, ...: two divisions in all
+// (one per 16-byte chunk made the first and last phases of a tile 3000 cycles
+// longer).
+struct RowWalk {
+  int qi, hl, dq, dh, group;
+  __device__ __forceinline__ RowWalk(int r, int step, int g) : group(g) {
+    qi = r / g;
+    hl = r - qi * g;
+    dq = step / g;
+    dh = step - dq * g;
+  }
+  __device__ __forceinline__ void next() {
+    qi += dq;
+    hl += dh;
+    if (hl >= group) {
+      hl -= group;
+      ++qi;
+    }
+  }
+};
+
 template <int D>
 struct Smem {
   static constexpr uint32_t kTile = CK * D * 2;  // one chunk of K (or V) in bf16
@@ -479,17 +500,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     if (nch > 0) {
       // Q tile: 16-byte chunks, all of a thread's in flight at once; rows past
       // the last are zeros
-      constexpr int NQ = QROWS * D / 8 / kSmx;
+      constexpr int NQ = QROWS * D / 8 / kSmx, STEP = kSmx / (D / 8);  // rows from one of a thread's chunks to the next
       const uint32_t q0 = smem_u32(smem + L::q);
       uint4 x[NQ];
+      RowWalk at(qt * QROWS + (int)threadIdx.x / (D / 8), STEP, a.group);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const int e = threadIdx.x + i * kSmx, row = e / (D / 8), ch = e % (D / 8), rq = qt * QROWS + row;
+        const int row = (int)threadIdx.x / (D / 8) + i * STEP, ch = threadIdx.x % (D / 8);
         x[i] = make_uint4(0, 0, 0, 0);
-        if (rq < rows) {
-          const int qi = rq / a.group, hl = rq - qi * a.group;
-          x[i] = *reinterpret_cast<const uint4*>(a.q + b * a.q_seq + qi * a.q_tok + (long long)(h * a.group + hl) * a.q_head + ch * 8);
-        }
+        if (qt * QROWS + row < rows)
+          x[i] = *reinterpret_cast<const uint4*>(a.q + b * a.q_seq + at.qi * a.q_tok + (long long)(h * a.group + at.hl) * a.q_head + ch * 8);
+        at.next();
       }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -703,17 +724,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     ok = rows_and(1 + (warp & 3), ok);
     if (ok) {
       // the four warps of these 32 rows take 8 rows each
-      const int cpr = (int)rowb / 16;  // chunks per row: 8 to 64
       const int base = (warp & 3) * 32 + part * 8;
-      for (int e = lane; e < 8 * cpr; e += 32) {
-        const int row = base + e / cpr, ch = e % cpr, q = qt * QROWS + row;
-        if (q >= rows) continue;
-        const uint4 x = lds128(stage + (uint32_t)row * rowb + (uint32_t)((ch ^ (row & 7)) << 4));
-        if (splits == 1) {
-          const int qi = q / a.group, hl = q - qi * a.group;
-          *reinterpret_cast<uint4*>(a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + ch * 8) = x;
-        } else {
-          *reinterpret_cast<uint4*>(a.part_o + (pr0 + row) * D + ch * 4) = x;
+      if (splits == 1) {
+        constexpr int CPR = D / 8, STEP = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide store
+        RowWalk at(qt * QROWS + base + lane / CPR, STEP, a.group);
+#pragma unroll
+        for (int i = 0; i < 8 / STEP; ++i) {
+          const int row = base + lane / CPR + i * STEP, ch = lane % CPR;
+          const uint4 x = lds128(stage + (uint32_t)row * rowb + (uint32_t)((ch ^ (row & 7)) << 4));
+          if (qt * QROWS + row < rows)
+            *reinterpret_cast<uint4*>(a.o + b * a.o_seq + at.qi * a.o_tok + (long long)(h * a.group + at.hl) * a.o_head + ch * 8) = x;
+          at.next();
+        }
+      } else {
+        constexpr int CPR = D / 4;
+#pragma unroll
+        for (int e = 0; e < 8 * CPR; e += 32) {
+          const int row = base + (e + lane) / CPR, ch = (e + lane) % CPR;
+          const uint4 x = lds128(stage + (uint32_t)row * rowb + (uint32_t)((ch ^ (row & 7)) << 4));
+          if (qt * QROWS + row < rows) *reinterpret_cast<uint4*>(a.part_o + (pr0 + row) * D + ch * 4) = x;
         }
       }
     }
