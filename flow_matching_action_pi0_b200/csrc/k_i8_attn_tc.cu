@@ -187,23 +187,26 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   return v;
 }
 
-// Query and head-in-group of the rows r, r + step, ...: two divisions in all
-// (one per 16-byte chunk made the first and last phases of a tile 3000 cycles
-// longer).
+// Offsets of the rows r, r + step, ... (row = query * group + head) of a
+// [token][head] layout: two divisions and products for all of them (per 16-byte
+// chunk they made the first and last phases of a tile 5000 cycles longer).
 struct RowWalk {
-  int qi, hl, dq, dh, group;
-  __device__ __forceinline__ RowWalk(int r, int step, int g) : group(g) {
-    qi = r / g;
+  long long at, step, wrap;
+  int hl, dh, group;
+  __device__ __forceinline__ RowWalk(int r, int rows_apart, int g, long long tok, long long head) : group(g) {
+    const int qi = (int)((unsigned)r / (unsigned)g), dq = (int)((unsigned)rows_apart / (unsigned)g);
     hl = r - qi * g;
-    dq = step / g;
-    dh = step - dq * g;
+    dh = rows_apart - dq * g;
+    at = qi * tok + hl * head;
+    step = dq * tok + dh * head;
+    wrap = tok - g * head;
   }
   __device__ __forceinline__ void next() {
-    qi += dq;
+    at += step;
     hl += dh;
     if (hl >= group) {
       hl -= group;
-      ++qi;
+      at += wrap;
     }
   }
 };
@@ -283,7 +286,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   const int r_last = min(rows, qt * QROWS + QROWS) - 1;
   const int seen = a.causal ? max(0, min(len, len - a.n_q + 1 + r_last / a.group)) : len;
   const int nc = (seen + CK - 1) / CK, nf = (a.n_new + CK - 1) / CK;
-  const int c0 = (int)((long long)(nc + nf) * split / splits), c1 = (int)((long long)(nc + nf) * (split + 1) / splits);
+  // (under 2^26 chunks, 1, 2, 4 or 8 splits; as 64-bit divisions by all threads
+  // the two took 1000 cycles)
+  const int sh = 31 - __clz(splits);
+  const int c0 = (int)(((uint32_t)(nc + nf) * split) >> sh), c1 = (int)(((uint32_t)(nc + nf) * (split + 1)) >> sh);
   const int nch = c1 - c0;
 
   if (warp >= kConvWarp) {
@@ -503,14 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       constexpr int NQ = QROWS * D / 8 / kSmx, STEP = kSmx / (D / 8);  // rows from one of a thread's chunks to the next
       const uint32_t q0 = smem_u32(smem + L::q);
       uint4 x[NQ];
-      RowWalk at(qt * QROWS + (int)threadIdx.x / (D / 8), STEP, a.group);
+      RowWalk walk(qt * QROWS + (int)threadIdx.x / (D / 8), STEP, a.group, a.q_tok, a.q_head);
+      const bf16* qp = a.q + b * a.q_seq + h * a.group * a.q_head + (threadIdx.x % (D / 8)) * 8;
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const int row = (int)threadIdx.x / (D / 8) + i * STEP, ch = threadIdx.x % (D / 8);
         x[i] = make_uint4(0, 0, 0, 0);
-        if (qt * QROWS + row < rows)
-          x[i] = *reinterpret_cast<const uint4*>(a.q + b * a.q_seq + at.qi * a.q_tok + (long long)(h * a.group + at.hl) * a.q_head + ch * 8);
-        at.next();
+        if (qt * QROWS + (int)threadIdx.x / (D / 8) + i * STEP < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(qp + walk.at));
+        walk.next();
       }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -727,14 +732,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       const int base = (warp & 3) * 32 + part * 8;
       if (splits == 1) {
         constexpr int CPR = D / 8, STEP = 32 / CPR;  // 16-byte chunks per row, rows per warp-wide store
-        RowWalk at(qt * QROWS + base + lane / CPR, STEP, a.group);
+        RowWalk walk(qt * QROWS + base + lane / CPR, STEP, a.group, a.o_tok, a.o_head);
+        bf16* op = a.o + b * a.o_seq + h * a.group * a.o_head + (lane % CPR) * 8;
 #pragma unroll
         for (int i = 0; i < 8 / STEP; ++i) {
           const int row = base + lane / CPR + i * STEP, ch = lane % CPR;
           const uint4 x = lds128(stage + (uint32_t)row * rowb + (uint32_t)((ch ^ (row & 7)) << 4));
-          if (qt * QROWS + row < rows)
-            *reinterpret_cast<uint4*>(a.o + b * a.o_seq + at.qi * a.o_tok + (long long)(h * a.group + at.hl) * a.o_head + ch * 8) = x;
-          at.next();
+          if (qt * QROWS + row < rows) *reinterpret_cast<uint4*>(op + walk.at) = x;
+          walk.next();
         }
       } else {
         constexpr int CPR = D / 4;
