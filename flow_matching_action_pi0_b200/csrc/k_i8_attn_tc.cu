@@ -30,6 +30,8 @@
 // and the cache's floors (K and V of a sequence are converted once per tile).
 // Key splits (small batches) write fp32 averages with the logarithm of their
 // weight to the workspace; k_kv8_merge joins them.
+#include <climits>
+
 #include <cuda_fp16.h>
 
 #include "int8.h"
@@ -57,34 +59,6 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;  // one instruction for the pair, round to nearest even
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// Two fp32 operations in one instruction: (a, b) op (c, d).
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-  return r;
-}
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-  float2 r;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%6, %7};\n\t"
-      "fma.rn.f32x2 c, a, b, d;\n\tmov.b64 {%0, %1}, c;\n\t}"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
   return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -397,7 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     // vs / 2^E in [1, 128) (c stays below 2^15), and the exponentials serve the
     // row sums too.  Others take log2 vs
     // key by key, so that a large row that a query does not see or weigh, or a
-    // zero one that it weighs most, costs the others nothing.
+    // zero one that it weighs most, costs the others nothing.  So do chunks that
+    // some of the tile's queries see in part: no bit of a result may depend on a
+    // key behind the query.
+    const int all_see = a.causal ? (len - a.n_q + 1 + qt * QROWS / a.group) & ~(CK - 1) : INT_MAX;
     float k[2], v[2];
     auto load = [&](int c) {
 #pragma unroll
@@ -421,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       const uint32_t b0 = __float_as_uint(v[0]), b1 = __float_as_uint(v[1]);
       const int hi = (int)(__reduce_max_sync(0xffffffffu, max(b0 & 0x7FFFFFFFu, b1 & 0x7FFFFFFFu)) >> 23);
       const int lo = (int)(__reduce_min_sync(0xffffffffu, min(b0, b1)) >> 23);
-      const bool narrow = hi < 255 && lo > 0 && hi - lo <= 6;
+      const bool narrow = hi < 255 && lo > 0 && hi - lo <= 6 && (c0 + i) * CK < all_see;
       const int e = narrow ? lo - 127 : 0;
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-E (-120 <= E <= 121)
       float* sl = s_sc + slot * kSc;

@@ -263,7 +263,7 @@ def test_cache_refuses_sizes_past_its_integers():
 # -------------------------------------------------------------- row quantiser
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-@pytest.mark.parametrize("rows,width", [(1, 1), (3, 7), (2, 1024), (5, 2047), (1, 4096), (1300, 512), (1201, 1024),
+@pytest.mark.parametrize("rows,width", [(1, 1), (3, 7), (2, 1024), (5, 2047), (1, 4096), (1300, 512), (1201, 1024), (8200, 512), (4100, 1000), (2100, 2048), (300, 256), (300, 496),
                                         (1190, 2048), (7, 16384), (3, 20000), (1500, 40)])
 def test_quantize_rows(rows, width, dtype):
     g = torch.Generator().manual_seed(rows * 31 + width)
@@ -436,6 +436,10 @@ CASES = [  # lens, capacity, kv heads, group, queries, fresh, causal, d
     ([200, 100, 20], 200, 1, 8, 40, 0, True, 256), ([300], 300, 3, 5, 31, 0, True, 128), ([129], 4096, 1, 8, 30, 0, True, 64),
     ([4096, 1000], 4096, 1, 2, 1, 0, False, 64), ([600], 600, 1, 8, 20, 130, False, 256), ([17], 64, 1, 17, 1, 0, False, 128),
     ([1500], 1500, 1, 1, 9, 0, True, 256), ([65, 1], 66, 4, 1, 130, 0, True, 64),
+    # on both sides of the choice between row groups and tiles
+    ([0, 64, 3] * 20, 64, 1, 2, 20, 0, False, 64), ([100, 1, 0] * 8, 100, 1, 8, 16, 0, False, 64), ([0, 40] * 12, 66, 4, 1, 130, 0, True, 64),
+    ([4096], 4096, 1, 8, 20, 0, False, 128), ([4096], 4096, 1, 8, 25, 0, True, 128), ([968] * 12, 968, 1, 8, 2, 0, False, 256),
+    ([968] * 12, 968, 1, 8, 3, 0, True, 256), ([20000, 1], 20000, 1, 8, 1, 0, False, 128),
 ]
 
 
@@ -462,7 +466,7 @@ def test_kv8_attention(lens, cap, hk, group, nq, fresh, causal, d):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("nq,group", [(4, 2), (40, 4)])
+@pytest.mark.parametrize("nq,group", [(4, 2), (40, 4), (130, 8)])
 def test_kv8_attention_causal_masks_nan_rows(nq, group):
     """A NaN row at position p reaches exactly the queries that may see p."""
     g = torch.Generator().manual_seed(nq)
@@ -481,7 +485,7 @@ def test_kv8_attention_causal_masks_nan_rows(nq, group):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("nq,fresh,causal", [(1, 0, False), (4, 0, True), (40, 0, False), (40, 33, False), (60, 0, True)])
+@pytest.mark.parametrize("nq,fresh,causal", [(1, 0, False), (4, 0, True), (40, 0, False), (40, 33, False), (60, 0, True), (160, 0, False)])
 def test_kv8_attention_rows_of_very_different_size(nq, fresh, causal):
     """Value rows from 2^-60 to 2^60 side by side (a row's weight decides, not
     its neighbours' size), zero rows, and huge rows where a query may not look."""
@@ -513,7 +517,7 @@ def test_kv8_attention_rows_of_very_different_size(nq, fresh, causal):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("nq,fresh", [(1, 0), (4, 0), (40, 0), (40, 33)])
+@pytest.mark.parametrize("nq,fresh", [(1, 0), (4, 0), (40, 0), (40, 33), (160, 0)])
 def test_kv8_attention_weight_on_empty_values(nq, fresh):
     """A key that takes nearly all the weight and has no value, or values of
     2^-90: what the others contribute keeps its precision."""
