@@ -126,10 +126,13 @@ __device__ __forceinline__ uint2 quant8(const float* f, float s, float inv) {
   uint32_t m[8];
   float worst = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float r = fmaf(f[i], inv, kMagic);
-    m[i] = __float_as_uint(r);
-    worst = fmaxf(worst, fabsf(fmaf(kMagic - r, s, f[i])));
+  for (int i = 0; i < 8; i += 2) {  // two at a time
+    const float2 x = make_float2(f[i], f[i + 1]);
+    const float2 r = fma2(x, make_float2(inv, inv), make_float2(kMagic, kMagic));
+    m[i] = __float_as_uint(r.x);
+    m[i + 1] = __float_as_uint(r.y);
+    const float2 e = fma2(add2(r, make_float2(-kMagic, -kMagic)), make_float2(-s, -s), x);
+    worst = fmaxf(worst, fmaxf(fabsf(e.x), fabsf(e.y)));
   }
   if (worst > s * 0.499999f) {
     int q[8];
@@ -149,8 +152,8 @@ __device__ __forceinline__ float rms_scale(float s, float inv, float mean_sq, fl
 }
 
 // ------------------------------------------------------------ row quantiser
-// TPR threads per row (32: a warp, 256: the block), NV groups of 8 elements
-// per thread in registers; width % 8 == 0, rows 16-byte aligned.
+// TPR threads per row (32 to 256), NV groups of 8 elements per thread in
+// registers; width % 8 == 0, rows 16-byte aligned.
 template <typename T, int TPR, int NV>
 __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, long long ldx, int rows, int width,
                                                        float rms_eps, int8_t* __restrict__ codes,
@@ -178,17 +181,19 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
 #pragma unroll
   for (int i = 0; i < NV; ++i) am = max(am, v[i].amax());
   am = __reduce_max_sync(0xFFFFFFFFu, am);
-  if constexpr (TPR > 32) {
+  constexpr int WPR = TPR / 32;                          // warps per row
+  const int w0 = (int)threadIdx.x / TPR * WPR;           // the row's first
+  if constexpr (WPR > 1) {
     if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = am;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < 8; ++w) am = max(am, s_max[w]);
+    for (int w = 0; w < WPR; ++w) am = max(am, s_max[w0 + w]);
   }
   const float s = row_scale(am);
   const float inv = inv_scale(s);
   const float unit = rms_unit(s, inv);
   int8_t* cr = codes + (size_t)row * width;
-  float ss = 0.f;
+  float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = lane + i * TPR;
@@ -198,21 +203,22 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
       Vec8<T>::put_codes(cr, c, width / 2, inv > 0.f ? quant8(f, s, inv) : make_uint2(0, 0));
       if (rms_eps > 0.f) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = f[j] * unit;
-          ss = fmaf(t, t, ss);
+        for (int j = 0; j < 8; j += 2) {
+          const float2 t = mul2(make_float2(f[j], f[j + 1]), make_float2(unit, unit));
+          ss2 = fma2(t, t, ss2);
         }
       }
     }
   }
+  float ss = 0.f;
   if (rms_eps > 0.f) {
-    ss = warp_sum(ss);
-    if constexpr (TPR > 32) {
+    ss = warp_sum(ss2.x + ss2.y);
+    if constexpr (WPR > 1) {
       if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = ss;
       __syncthreads();
       ss = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) ss += s_sum[w];
+      for (int w = 0; w < WPR; ++w) ss += s_sum[w0 + w];
     }
   }
   if (live && lane == 0) scale[row] = rms_eps > 0.f ? rms_scale(s, inv, ss / (float)width, rms_eps) : s;
@@ -272,15 +278,20 @@ cudaError_t quant_sel(const void* x, long long ldx, int rows, int width, float e
   if (!vec || nv > 256 * 8)
     return launch_ex(k_quantize_rows_any<T>, dim3(rows), dim3(256), 0, st, 1, true, static_cast<const T*>(x), ldx, rows,
                      width, eps, codes, scale);
-  // A warp per row while its registers hold the row; a block per row when the
-  // row is longer, or when so few rows would leave most SMs idle.
-  constexpr int kWarpNv = sizeof(T) == 2 ? 8 : 4;
-  if (nv <= 32 * kWarpNv && rows >= 148 * 8) {
-    if (nv <= 64) return quant_launch<T, 32, 2>(x, ldx, rows, width, eps, codes, scale, st);
-    if (nv <= 128) return quant_launch<T, 32, 4>(x, ldx, rows, width, eps, codes, scale, st);
-    return quant_launch<T, 32, kWarpNv>(x, ldx, rows, width, eps, codes, scale, st);
+  // As many threads as the row has groups, up to a block: a row is then one round
+  // trip (1600 rows of 2048 bf16: 9.6 us with a warp per row, 4.8 with a block).
+  // Where the rows fill the SMs more than once anyway, two groups per thread halve
+  // the reductions (20000 rows of 1024: 19.8 us with one, 16.7 with two; 4000: 5.5
+  // and 5.6; 2000: 3.7 and 4.7).
+  if ((long long)rows * nv < (1 << 19)) {
+    if (nv > 32 && nv <= 64) return quant_launch<T, 64, 1>(x, ldx, rows, width, eps, codes, scale, st);
+    if (nv > 64 && nv <= 128) return quant_launch<T, 128, 1>(x, ldx, rows, width, eps, codes, scale, st);
+    if (nv > 128 && nv <= 256) return quant_launch<T, 256, 1>(x, ldx, rows, width, eps, codes, scale, st);
   }
-  if (nv <= 256) return quant_launch<T, 256, 1>(x, ldx, rows, width, eps, codes, scale, st);
+  if (nv <= 32) return quant_launch<T, 32, 1>(x, ldx, rows, width, eps, codes, scale, st);
+  if (nv <= 64) return quant_launch<T, 32, 2>(x, ldx, rows, width, eps, codes, scale, st);
+  if (nv <= 128) return quant_launch<T, 64, 2>(x, ldx, rows, width, eps, codes, scale, st);
+  if (nv <= 256) return quant_launch<T, 128, 2>(x, ldx, rows, width, eps, codes, scale, st);
   if (nv <= 512) return quant_launch<T, 256, 2>(x, ldx, rows, width, eps, codes, scale, st);
   return quant_launch<T, 256, 8>(x, ldx, rows, width, eps, codes, scale, st);
 }
