@@ -542,13 +542,13 @@ __device__ __forceinline__ void merge_part(float2 ml, float4 x, float& m, float&
 
 // Joins the parts of the (sequence, KV head, row group) items that
 // k_kv8_attn_few left to several blocks: one block per (row, item).
-template <int D>
-__global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int rgs, int blocks) {
-  constexpr int C4 = D / 4, NS = 256 / C4;
-  __shared__ long long s_scan[8];
+template <int D, int NT>
+__global__ void __launch_bounds__(NT) k_kv8_merge_few(const Kv8AttnArgs a, int rgs, int blocks) {
+  constexpr int C4 = D / 4, NS = NT / C4;
+  __shared__ long long s_scan[NT / 32];
   __shared__ long long s_before;
   __shared__ float2 s_ml[NS];
-  __shared__ float4 s_acc[256];
+  __shared__ float4 s_acc[NT];
   const int item_all = blockIdx.x, r = blockIdx.y;  // ((sequence, KV head), row group); row of the group
   const int hr = a.c.heads * rgs, b = item_all / hr, item = item_all - b * hr;
   const int h = item / rgs, rg = item - h * rgs;
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(256) k_kv8_merge_few(const Kv8AttnArgs a, int 
   {
     int b0, b1;
     long long before;
-    total = scan_units<256>(a, s_scan, b0, b1, before) * hr;
+    total = scan_units<NT>(a, s_scan, b0, b1, before) * hr;
     for (int i = b0; i < b1; ++i) {
       if (i == b) s_before = before;
       before += seq_units(seq_len(a, i));
@@ -642,8 +642,12 @@ template <int D>
 cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cudaStream_t st) {
   cudaError_t e = launch_ex(k_kv8_attn_few<D>, dim3(p.splits), dim3(kWarps * 32), few_smem(D), st, 1, pdl, a, p.qtiles);
   if (e != cudaSuccess || p.ws_bytes == 0) return e;
-  return launch_ex(k_kv8_merge_few<D>, dim3(a.n_seq * a.c.heads * p.qtiles, 8), dim3(256), 0, st, 1, true, a, p.qtiles,
-                   p.splits);
+  // twice the threads where an item may have more than 32 parts (one sequence of
+  // 65536 keys: 27.0 us with 256, 19.8 with 512; 32 of 968 and two row groups: 16.6
+  // and 19.9)
+  const dim3 items(a.n_seq * a.c.heads * p.qtiles, 8);
+  if (p.splits > 32LL * items.x) return launch_ex(k_kv8_merge_few<D, 512>, items, dim3(512), 0, st, 1, true, a, p.qtiles, p.splits);
+  return launch_ex(k_kv8_merge_few<D, 256>, items, dim3(256), 0, st, 1, true, a, p.qtiles, p.splits);
 }
 template <int D>
 cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {  // (PDL behind its own attention)
@@ -654,32 +658,39 @@ cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_
 
 }  // namespace
 
-// Rows of a KV head (query heads in its group x queries): up to 16 take groups
-// of 8 rows on mma.sync, more (or any fresh keys) tiles of 128 rows on the
-// tcgen05 tensor cores, whose keys are split until the CTAs fill the SMs,
-// each split keeping at least 64 keys of a full cache.
+// Two forms: groups of 8 rows (query heads of a KV head x queries) on mma.sync,
+// which read the cache once per group, and tiles of 128 rows on the tcgen05
+// tensor cores (fresh keys always), whose keys are split until the CTAs fill
+// the SMs, each split keeping at least 64 keys of a full cache (one sequence of
+// 968 keys and 400 rows: 12.6 us; 14.8 with at least 128, 20.2 with 256).
+// Measured over 1 to 32 sequences of 256 to 16384 keys, 8 to 256 rows, head_dim d:
+//   groups  5.4 + d / 100 us, and 3.2 + d / 80 ns per unit (64 keys of 8 rows)
+//   tiles   4.7 + d / 100 us, and 1.0 + d / 570 us per chunk of 64 keys that a CTA
+//           walks
+// e.g. (d 256) 32 rows over 968 keys: 8.0 and 10.9 us for 1 sequence, 13.5 and 11.3
+// for 8; 8 rows, 32 sequences: 13.5 and 14.9; 64 rows over 4096 keys: 11.9 and 19.6
+// for 1, 53.5 and 22.2 for 16.
 Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new, int max_keys, int d) {
-  Kv8AttnPlan p{};
-  const long long rows = (long long)group * n_q;
-  p.tc = rows > 16 || n_new > 0;
-  const int tile = p.tc ? 128 : 8;
-  p.qtiles = (int)((rows + tile - 1) / tile);
-  const long long blocks = (long long)n_seq * heads_kv * p.qtiles;
+  const long long rows = (long long)group * n_q, seqs = (long long)n_seq * heads_kv;
+  Kv8AttnPlan t{};  // tiles
+  t.tc = 1;
+  t.qtiles = (int)((rows + 127) / 128);
+  const long long blocks = seqs * t.qtiles;
   const int keys = std::max(1, max_keys + n_new);
-  int splits = 1;
-  if (!p.tc) {
-    // blocks that deal out the units of 64 keys: two (four for head_dim < 256)
-    // resident per SM, and no more than there are units in a full cache
-    const long long units = blocks * ((std::max(max_keys, 1) - 1) / kUnit + 1);
-    p.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
-    // (with one unit per item no item is shared)
-    p.ws_bytes = p.splits > 1 && units > blocks ? (size_t)p.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
-    return p;
-  }
-  while (splits < 8 && blocks * splits * 2 <= 148 && keys / (splits * 2) >= 64) splits *= 2;
-  p.splits = splits;
-  p.ws_bytes = splits > 1 ? (size_t)blocks * splits * tile * ((size_t)d * 4 + 8) : 0;
-  return p;
+  t.splits = 1;
+  while (t.splits < 8 && blocks * t.splits * 2 <= 148 && keys / (t.splits * 2) >= 64) t.splits *= 2;
+  t.ws_bytes = t.splits > 1 ? (size_t)blocks * t.splits * 128 * ((size_t)d * 4 + 8) : 0;
+  const long long chunks = ((keys - 1) / 64 + t.splits) / t.splits * ((blocks * t.splits + 147) / 148);
+
+  Kv8AttnPlan g{};  // groups
+  g.qtiles = (int)((rows + 7) / 8);
+  // blocks that deal out the units: two (four for head_dim < 256) resident per
+  // SM, and no more than there are units in a full cache
+  const long long units = seqs * g.qtiles * ((std::max(max_keys, 1) - 1) / kUnit + 1);
+  g.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
+  // (with one unit per item no item is shared)
+  g.ws_bytes = g.splits > 1 && max_keys > kUnit ? (size_t)g.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
+  return n_new == 0 && 700 + (3.2 + d / 80.0) * (double)units < (1010 + 1.75 * d) * (double)chunks ? g : t;
 }
 
 cudaError_t kv8_attn_init() {
