@@ -38,7 +38,7 @@
 // out evenly: block i of G takes units [T i / G, T (i + 1) / G), whatever the
 // lengths, so a batch of ragged sequences finishes together (an equal number
 // of splits per sequence left the SMs to the longest ones: 36.8 us for 48
-// sequences of up to 8192 keys).  Inside a block each warp has statistics of
+// sequences of up to 8192 keys, 31.5 now, 3.3 TB/s).  Inside a block each warp has statistics of
 // its own and the warps meet once per sequence.  A sequence that lies in one
 // block is written out by it; of the others each block parks its fp32 rows in
 // one of its two workspace slots (0: the part continues an earlier block's, 1:

@@ -26,8 +26,10 @@
 //                         chunk-to-chunk chain runs through it, so its latency
 //                         counts: with two threads per row a chunk took 2900
 //                         cycles.
-// Bound: the softmax and conversion work per tile, between the tensor cores'
-// and the cache's floors (K and V of a sequence are converted once per tile).
+// Bound: the latency of that chain, 2600 cycles per chunk (the tensor cores are
+// busy for 1050 of them, the issue slots for about half): 50 queries x 8 heads of
+// 32 sequences over 968 + 50 keys, 128 CTAs of 17 chunks, 32 us; K and V of a
+// sequence are converted once per tile.
 // Key splits (small batches) write fp32 averages with the logarithm of their
 // weight to the workspace; k_kv8_merge joins them.
 #include <climits>
