@@ -412,14 +412,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NB; ++i) {
           const int c = b0 + i;
           if (c >= nc) break;
+          // (sum sx) sw, as for few tokens: a product of the scales alone may be subnormal
           float o[16];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
-            o[4 * q] = (float)acc[i][4 * q] * (sx * w.x);
-            o[4 * q + 1] = (float)acc[i][4 * q + 1] * (sx * w.y);
-            o[4 * q + 2] = (float)acc[i][4 * q + 2] * (sx * w.z);
-            o[4 * q + 3] = (float)acc[i][4 * q + 3] * (sx * w.w);
+            o[4 * q] = (float)acc[i][4 * q] * sx * w.x;
+            o[4 * q + 1] = (float)acc[i][4 * q + 1] * sx * w.y;
+            o[4 * q + 2] = (float)acc[i][4 * q + 2] * sx * w.z;
+            o[4 * q + 3] = (float)acc[i][4 * q + 3] * sx * w.w;
           }
           if (!a.tma_out) {
             if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);

@@ -363,6 +363,22 @@ def test_linear_i8_sums_reach_32_bits(tokens):
     assert torch.equal(y.cpu(), want.float().expand(tokens, 5))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [3, 200, 600])
+def test_linear_i8_small_scales(tokens):
+    """Scales whose product is subnormal (1.37 2^-80, 1.61 2^-60) and sums that
+    bring the result back: two fp32 products of a whole number below 2^24 with
+    normal results are off by half a step each, 2^-23 in all (and 2^-47)."""
+    k, n = 512, 300
+    g = torch.Generator().manual_seed(tokens)
+    x, w = torch.randint(100, 128, (tokens, k), generator=g), torch.randint(100, 128, (n, k), generator=g)
+    sx, sw = torch.full((tokens,), 1.37 * 2.0 ** -80), torch.full((n,), 1.61 * 2.0 ** -60)
+    want = (x.double() @ w.double().t()) * sx.double()[:, None] * sw.double()
+    assert float((x.double() @ w.double().t()).max()) < 2 ** 24
+    got = fm.linear_i8(x.to(torch.int8).cuda(), sx.cuda(), w.to(torch.int8).cuda(), sw.cuda(), out_dtype=torch.float32)
+    assert bool(((got.cpu().double() - want).abs() <= want * (2.0 ** -23 + 2.0 ** -46)).all())
+
+
 # ------------------------------------------------------------------- K/V cache
 def _cu(lens):
     return torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
