@@ -370,14 +370,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Thread = row; the two warps of a lane quarter take the 128-byte boxes of
     // columns in turn.  A box goes through the warp's 4 KB buffer (32 rows,
     // swizzled) and leaves as one bulk tensor store, which clips at the matrix's
-    // edges; outputs that a tensor map cannot describe are stored from the
-    // registers.
+    // edges.  Outputs that a tensor map cannot describe leave from the registers in
+    // 16-byte stores, or, where their rows start off 16 bytes, element by element
+    // along the rows of the buffer (a lane's own row in single elements is 32 rows
+    // per store: 3997 x 9999 x 1024: fp32 275 us so, 81 now; bf16 375 and 56).
     constexpr int CPB = 128 / (int)sizeof(TO), NB = CPB / 16;  // columns and 16-column chunks per box
     const int et = threadIdx.x - 128, half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t box = smem_u32(smem + L.out_off) + (uint32_t)(warp - 4) * 4096u;
     TO* y = static_cast<TO*>(a.y);
     const bool vec = (reinterpret_cast<uintptr_t>(y) & 15) == 0 && (a.ldy * (long long)sizeof(TO)) % 16 == 0;
+    const bool staged = a.tma_out || !vec;
     const int nc = p.tn / 16;
     int n = 0;
     for (int tile = first; tile < tiles; tile += step, ++n) {
@@ -422,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[4 * q + 2] = (float)acc[i][4 * q + 2] * sx * w.z;
             o[4 * q + 3] = (float)acc[i][4 * q + 3] * sx * w.w;
           }
-          if (!a.tma_out) {
+          if (!staged) {
             if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
             continue;
           }
@@ -453,6 +456,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (x < a.n && yr < a.tokens) tma_store_2d(&tmY, box, x, yr);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
+        } else if (staged) {  // row by row, element by element
+          __syncwarp();
+          const int rows = min(32, a.tokens - row0 - (warp & 3) * 32), cols = min(min(CPB, (nc - b0) * 16), a.n - f0 - b0 * 16);
+          TO* yr = y + (size_t)(row0 + (warp & 3) * 32) * a.ldy + f0 + b0 * 16;
+          for (int r = 0; r < rows; ++r, yr += a.ldy)
+#pragma unroll
+            for (int c = lane; c < CPB; c += 32) {
+              const int at = c * (int)sizeof(TO);
+              const TO v = *reinterpret_cast<const TO*>(smem + L.out_off + (warp - 4) * 4096 + r * 128 + ((((at >> 4) ^ (r & 7)) << 4) | (at & 15)));
+              if (c < cols) yr[c] = v;
+            }
+          __syncwarp();
         }
       }
       // this CTA's epilogue warps are done with the accumulator
