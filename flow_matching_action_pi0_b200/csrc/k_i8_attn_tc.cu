@@ -668,8 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       l += x == -INFINITY ? s_l[p * QROWS + r] : s_l[p * QROWS + r] * ex2(x - X);
     }
     const float lw = X == -INFINITY ? l : X + __log2f(l);
-    // O in units of 2^ref -> the average over the keys; no visible key: zeros
-    const float inv = l == 0.f ? 0.f : ex2(ref - lw);
+    // O in units of 2^ref -> the average over the keys; no visible key, or none
+    // with a value (ref is then not set, O is 0, or NaN of a NaN value scale): zeros
+    const float inv = l == 0.f || (!has && l == l) ? 0.f : ex2(ref - lw);
     // Output rows go through shared memory (every MMA is done: the tiles are
     // free), so that a row leaves as one run of 16-byte stores; straight from
     // the registers, a warp's store touches 32 rows and the 128 rows of a tile
