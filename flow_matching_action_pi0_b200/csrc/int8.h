@@ -101,11 +101,14 @@ cudaError_t launch_kv8_write(bool bf16_rows, const Kv8& c, const Kv8Rows& r, con
 cudaError_t launch_kv8_read(bool bf16_rows, const Kv8& c, const Kv8Rows& r, const Kv8Io& io, cudaStream_t st);
 
 // ---------------------------------------------------------------- attention
-constexpr int kMaxKv8Splits = 8;
+// Keys that share the units of one reference at most (a tile's part, a warp's
+// share of a row group): contributions in fp16 are off by 2^-28 of the row's
+// largest each on tiles, 2^-32 in row groups, 2^-11 of it for all of them.
+constexpr long long kTileRefKeys = 1 << 17, kGroupRefKeys = 1 << 21;
 struct Kv8AttnPlan {
   int tc;        // 1: tcgen05 tiles of 128 query rows; 0: groups of 8 rows
   int qtiles;    // row tiles (tc) or row groups per (sequence, KV head)
-  int splits;    // tc: key splits; > 1: partial rows go to the workspace and are merged by a second launch
+  int splits;    // tc: key splits (a power of two); > 1: partial rows go to the workspace and are merged by a second launch
                  // not tc: blocks that share the keys of all sequences; ws_bytes > 0: merged likewise
   size_t ws_bytes;
 };

@@ -13,9 +13,10 @@
 // integers, exactly, and the value's scale joins the exponent:
 //   c_j = exp2(s_j + log2 vs_j - ref) = p_j vs_j 2^(m - ref),
 // so that c in fp16 (rounded once, to 11 bits) is in units of the row's largest
-// contribution whatever the scales are: max c lies in [1, 256], and what falls
-// under fp16's 2^-24 is less than the largest one's own code step by far.  The
-// row sums have a reference m of their own, since a key may weigh much and
+// contribution whatever the scales are: max c lies in [2^7, 2^15], so the steps of
+// 2^-24 at fp16's bottom put each contribution off by at most 2^-32 of the largest,
+// and the n keys of a warp's share by n 2^-32 at worst (all of them below the
+// step: the row sum counts what they lose).  The row sums have a reference m of their own, since a key may weigh much and
 // carry little: sum p_j in fp32, lane by lane.  The two meet in the exponent of
 // the row's last factor, 2^(ref - m) / sum, and partial rows are parked as
 // averages with the logarithm of their weight, so no size of V overflows.
@@ -57,6 +58,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTileKeys = 16;
+constexpr float kLift = 7.f, kTop = 15.f;  // log2 of the largest c where the reference is set, and where it moves
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -385,10 +387,10 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
-      // the reference moves only when the maximum grows by more than 8 (a
-      // factor 256): c stays below 256 and O is rescaled rarely
-      const bool up = mx > m_run[i] + 8.f || m_run[i] == -INFINITY;
-      const float nm = up ? fmaxf(mx, m_run[i]) : m_run[i];
+      // the reference moves only when the maximum grows by a factor 256 above
+      // where it was set: c stays within 2^15 and O is rescaled rarely
+      const bool up = mx > m_run[i] + kTop || m_run[i] == -INFINITY;
+      const float nm = up ? fmaxf(mx - kLift, m_run[i]) : m_run[i];
       al[i] = nm == -INFINITY ? 1.f : ex2(m_run[i] - nm);
       grow |= al[i] != 1.f;
       m_run[i] = nm;
@@ -617,19 +619,25 @@ __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int spli
   if (row >= a.group * a.n_q) return;
   const int b = bg / a.c.heads, h = bg - b * a.c.heads;
   const size_t p0 = (size_t)bg * splits * rowsp + row;
-  float2 ml[kMaxKv8Splits];
-  float4 x[kMaxKv8Splits];
-#pragma unroll
-  for (int s = 0; s < kMaxKv8Splits; ++s)
-    if (s < splits) {
-      ml[s] = __ldcg(a.part_ml + p0 + (size_t)s * rowsp);
-      x[s] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (p0 + (size_t)s * rowsp) * D + 4 * c4));
-    }
+  constexpr int NP = 8;  // parts in flight
   float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto join = [&](int s0) {
+    float2 ml[NP];
+    float4 x[NP];
 #pragma unroll
-  for (int s = 0; s < kMaxKv8Splits; ++s)
-    if (s < splits) merge_part(ml[s], x[s], m, l, acc);
+    for (int s = 0; s < NP; ++s)
+      if (s0 + s < splits) {
+        const size_t at = p0 + (size_t)(s0 + s) * rowsp;
+        ml[s] = __ldcg(a.part_ml + at);
+        x[s] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + 4 * c4));
+      }
+#pragma unroll
+    for (int s = 0; s < NP; ++s)
+      if (s0 + s < splits) merge_part(ml[s], x[s], m, l, acc);
+  };
+  join(0);
+  for (int s0 = NP; s0 < splits; s0 += NP) join(s0);
   const int qi = row / a.group, hl = row - qi * a.group;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
@@ -676,18 +684,21 @@ Kv8AttnPlan plan_kv8_attn(int n_seq, int heads_kv, int group, int n_q, int n_new
   t.tc = 1;
   t.qtiles = (int)((rows + 127) / 128);
   const long long blocks = seqs * t.qtiles;
-  const int keys = std::max(1, max_keys + n_new);
+  const long long keys = std::max(1LL, (long long)max_keys + n_new);
   t.splits = 1;
   while (t.splits < 8 && blocks * t.splits * 2 <= 148 && keys / (t.splits * 2) >= 64) t.splits *= 2;
+  while (keys > kTileRefKeys * t.splits) t.splits *= 2;
   t.ws_bytes = t.splits > 1 ? (size_t)blocks * t.splits * 128 * ((size_t)d * 4 + 8) : 0;
   const long long chunks = ((keys - 1) / 64 + t.splits) / t.splits * ((blocks * t.splits + 147) / 148);
 
   Kv8AttnPlan g{};  // groups
   g.qtiles = (int)((rows + 7) / 8);
   // blocks that deal out the units: two (four for head_dim < 256) resident per
-  // SM, and no more than there are units in a full cache
+  // SM, more where a warp's share of a full cache would be too long for one
+  // reference, and no more than there are units in it
   const long long units = seqs * g.qtiles * ((std::max(max_keys, 1) - 1) / kUnit + 1);
-  g.splits = (int)std::min<long long>(units, 148LL * (d == 256 ? 2 : 4));
+  const long long shares = (units * kTileKeys - 1) / kGroupRefKeys + 1;
+  g.splits = (int)std::min<long long>(units, std::max(148LL * (d == 256 ? 2 : 4), shares));
   // (with one unit per item no item is shared)
   g.ws_bytes = g.splits > 1 && max_keys > kUnit ? (size_t)g.splits * 2 * 8 * ((size_t)d * 4 + 8) : 0;
   return n_new == 0 && 700 + (3.2 + d / 80.0) * (double)units < (1010 + 1.75 * d) * (double)chunks ? g : t;

@@ -51,6 +51,14 @@ constexpr int kConv = 128;                 // converter threads per operand
 constexpr int kThreads = kConvWarp * 32 + 2 * kConv;
 constexpr int KP = CK / 4;                 // keys per softmax part
 constexpr int kSc = 2 * CK + 4;            // a chunk's scales: ks [64], vs' or log2 vs [64], (narrow, E)
+// The reference of a row's contributions is set kLift below the largest one and
+// moves once one exceeds it by kTop.  fp16 holds c in steps of 2^-24 at the bottom,
+// an error of 2^-25 at most, so in units of the largest contribution each is off by
+// at most 2^-(25 + kLift): n of them, all of the same sign, by n times that (the row
+// sum counts what they lose).  kTileRefKeys (int8.h) bounds n.  At the top c stays below
+// 2^(kTop + 1 + kSpread), in fp16.
+constexpr float kLift = 3.f, kTop = 11.f;
+constexpr int kSpread = 3;                 // of a narrow chunk's value scales, see the scale warp
 constexpr long long kDrainNs = 4000000000LL;
 
 __device__ __forceinline__ float ex2(float x) {
@@ -262,10 +270,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
   const int r_last = min(rows, qt * QROWS + QROWS) - 1;
   const int seen = a.causal ? max(0, min(len, len - a.n_q + 1 + r_last / a.group)) : len;
   const int nc = (seen + CK - 1) / CK, nf = (a.n_new + CK - 1) / CK;
-  // (under 2^26 chunks, 1, 2, 4 or 8 splits; as 64-bit divisions by all threads
-  // the two took 1000 cycles)
+  // (a power of two splits; as 64-bit divisions by all threads the two took 1000
+  // cycles)
   const int sh = 31 - __clz(splits);
-  const int c0 = (int)(((uint32_t)(nc + nf) * split) >> sh), c1 = (int)(((uint32_t)(nc + nf) * (split + 1)) >> sh);
+  const int c0 = (int)(((unsigned long long)(nc + nf) * split) >> sh), c1 = (int)(((unsigned long long)(nc + nf) * (split + 1)) >> sh);
   const int nch = c1 - c0;
 
   if (warp >= kConvWarp) {
@@ -368,9 +376,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     // flight; a slot is written again only after its chunk's PV
     const size_t base = ((size_t)b * a.c.heads + h) * a.c.cap;
     //
-    // A chunk whose value scales lie within a factor 64 of one another takes the
+    // A chunk whose value scales lie within a factor 8 of one another takes the
     // smallest one's exponent E for all: c = exp2(s ks + E - ref) vs', vs' =
-    // vs / 2^E in [1, 128) (c stays below 2^15), and the exponentials serve the
+    // vs / 2^E in [1, 16) (c stays below 2^15), and the exponentials serve the
     // row sums too.  Others take log2 vs
     // key by key, so that a large row that a query does not see or weigh, or a
     // zero one that it weighs most, costs the others nothing.  So do chunks that
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       const uint32_t b0 = __float_as_uint(v[0]), b1 = __float_as_uint(v[1]);
       const int hi = (int)(__reduce_max_sync(0xffffffffu, max(b0 & 0x7FFFFFFFu, b1 & 0x7FFFFFFFu)) >> 23);
       const int lo = (int)(__reduce_min_sync(0xffffffffu, min(b0, b1)) >> 23);
-      const bool narrow = hi < 255 && lo > 0 && hi - lo <= 6 && (c0 + i) * CK < all_see;
+      const bool narrow = hi < 255 && lo > 0 && hi - lo <= kSpread && (c0 + i) * CK < all_see;
       const int e = narrow ? lo - 127 : 0;
       const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-E (-120 <= E <= 121)
       float* sl = s_sc + slot * kSc;
@@ -529,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       // visible keys of this part's
       const int vis = (c < nc ? lim - c * CK : a.n_new - (c - nc) * CK) - part * KP;
       // Exponents in units of the row's reference: y = s ks + E - ref.  The reference
-      // (a running maximum) moves only when an exponent of c exceeds it by more
-      // than 8, a factor 256, so that O is rescaled rarely; until then no part
+      // moves only when an exponent of c exceeds it by more than kTop, a factor 256
+      // above where it was set, so that O is rescaled rarely; until then no part
       // needs another part's maximum, only everyone's word that it stays.
       float2* s2 = reinterpret_cast<float2*>(sv);
       const float2 nref = make_float2(ch.y - ref, ch.y - ref);
@@ -557,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       // A part that must stop asks for a move too, so all meet below.
       const bool mine = got && s_flag[0] == 0;
       float alpha = 1.f;
-      if (rows_or(1 + (warp & 3), !mine || (has ? pmax > 8.f : pmax != -INFINITY))) {
+      if (rows_or(1 + (warp & 3), !mine || (has ? pmax > kTop : pmax != -INFINITY))) {
         float* pm = s_pm + r;
         pm[part * QROWS] = pmax;
         if (!rows_and(1 + (warp & 3), mine)) {
@@ -565,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
           break;
         }
         const float cmax = fmaxf(max3(pm[0], pm[QROWS], pm[2 * QROWS]), pm[3 * QROWS]);
-        const bool move = has ? cmax > 8.f : cmax != -INFINITY;  // (NaN alone: the reference stays)
-        const float up = move && cmax == cmax ? cmax : 0.f;
+        const bool move = has ? cmax > kTop : cmax != -INFINITY;  // (NaN alone: the reference stays)
+        const float up = move && cmax == cmax ? cmax - kLift : 0.f;
         ref += up;
         xmax -= up;
         alpha = has ? ex2(-up) : 1.f;

@@ -61,3 +61,33 @@ def test_values_of_zero_under_low_scores(nq, cap, zeros, causal):
     c.v_scale[0, 0, 0] = math.nan
     sees = slice(max(0, nq - cap) if causal else 0, nq)
     assert bool(torch.isnan(c.attend(q.cuda(), _lens(cap), causal=causal)[:, sees]).all())
+
+
+# ------------------------------------------------------------------ long tails
+@pytest.mark.gpu
+@pytest.mark.parametrize("below", [25.4, 27.5])
+@pytest.mark.parametrize("nq,cap", [(600, 1 << 20), (1, 1 << 20)])
+def test_a_long_tail_of_small_weights(nq, cap, below):
+    """One key takes nearly all the weight, 2^20 others 2^-25.4 or 2^-27.5 of it
+    each: together 2.4 % or 0.6 %, with values of the other sign.
+
+    A contribution is held in steps of 2^-27 of the row's largest at worst, an
+    error of 2^-28 each, and at most 2^17 keys share a reference; the parts of
+    others are in units of their own largest: 2^-11 of sum p |v| in all."""
+    d, group = 64, 16
+    c = fm.KvCacheInt8(1, 1, cap, d)
+    c.v.fill_(127)
+    c.v[0, 0, 0] = -127
+    c.v_scale.fill_(2.0 ** -7)
+    c.k_scale.fill_(2.0 ** -5)
+    q = torch.full((1, nq, group, d), 1.0, dtype=torch.bfloat16, device="cuda")
+    scale = below * math.log(2.0) / (64 * 64 * 2.0 ** -5)
+    c.k[0, 0, 0] = 64  # its score: 64 channels x 64 codes
+    got = c.attend(q, _lens(cap), scale=scale).double()
+    s = float(np.float32(scale)) * 64 * 64 * 2.0 ** -5  # log of the first key's weight
+    tail = (cap - 1) * math.exp(-s)
+    value = 127 * 2.0 ** -7
+    want = value * (tail - 1) / (tail + 1)
+    # (assert_attention's bound with the fp16 rounding of a probability, not bf16's)
+    tol = value * (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) + abs(want) * 2.0 ** -8
+    assert float((got - want).abs().max()) <= tol, (float(got.min()), float(got.max()), want)
