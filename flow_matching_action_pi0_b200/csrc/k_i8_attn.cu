@@ -5,11 +5,15 @@
 //   k_j = kq_j ks_j, v_j = vq_j vs_j  (8-bit codes, one scale per key)
 //
 // One pass over the keys with the running maximum and sum of a softmax.
-// Scores: a query row becomes 16-bit integers of its own scale, q = (256 hi +
-// lo) qs with two signed 8-bit digits, |q| error at most max|q| 2^-16, so the
-// key codes go into integer products as they lie in memory, two per 32
+// Scores: a query row becomes integers of a power of two qs, q = (2^16 hi + 2^8
+// mid + lo) qs with three signed 8-bit digits and 2^21 <= max|q| / qs < 2^22, so the
+// key codes go into integer products as they lie in memory, three per 32
 // channels, and the sums are exact.  (As bf16 operands every pair of codes
-// costs four instructions, half of the loop.)  Values: the codes become fp16
+// costs four instructions, half of the loop.)  An element is exact unless it is
+// below 2^-14 of the row's largest, and off by 2^-22 of that at most: no more than
+// an fp32 sum of the products may be.  (Two digits, 2^-16, took 32.1
+// instead of 33.0 us for 48 sequences of up to 8192 keys, but lost the small
+// channels of rows with a large one.)  Values: the codes become fp16
 // integers, exactly, and the value's scale joins the exponent:
 //   c_j = exp2(s_j + log2 vs_j - ref) = p_j vs_j 2^(m - ref),
 // so that c in fp16 (rounded once, to 11 bits) is in units of the row's largest
@@ -266,8 +270,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       sc_next[i] = scales(at + i * STEP);
     }
 
-  uint32_t qh[KBLK][4], ql[KBLK][4];  // digits of 4 channels per word
-  float qs[2];                        // scales of rows 2t, 2t + 1
+  uint32_t qh[KBLK][4], qm[KBLK][4], ql[KBLK][4];  // digits of 4 channels per word
+  float qs[2];                                     // scales of rows 2t, 2t + 1
   {
     uint32_t am = 0;
 #pragma unroll
@@ -280,15 +284,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     am = max(am << 16, am & 0xFFFF0000u);
     am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
     am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    // rows below 2^-110 count as zeros; a NaN or an infinity makes every score NaN
-    const bool some = am >= 0x08800000u && am < 0x7F800000u;
-    const float amax = __uint_as_float(am);
-    const float inv = some ? 32639.f / amax : 0.f;  // 127 * 256 + 127
-    const float sc = am >= 0x7F800000u ? __int_as_float(0x7FC00000) : some ? amax * (1.f / 32639.f) : 0.f;
+    // rows below 2^-105 count as zeros; a NaN or an infinity makes every score NaN
+    const uint32_t e = am >> 23;
+    const bool some = e >= 22 && e < 255;
+    const float inv = some ? __uint_as_float((275 - e) << 23) : 0.f;  // 2^21 / 2^(e - 127)
+    const float sc = e == 255 ? __int_as_float(0x7FC00000) : some ? __uint_as_float((e - 21) << 23) : 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) qs[i] = __shfl_sync(0xFFFFFFFFu, sc, (2 * t + i) * 4) * a.scale_log2;
-    // q inv + (1.5 2^23 + 128) rounds to a whole number in the low bits of the
-    // sum: byte 1 is hi, byte 0 is lo + 128
+    // q inv + 1.5 2^23 rounds to a whole number in the low bits of the sum; that
+    // number + 0x8080 has hi in byte 2, mid + 128 in byte 1 and lo + 128 in byte 0
 #pragma unroll
     for (int j = 0; j < KBLK; ++j)
 #pragma unroll
@@ -298,8 +302,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
                             __uint_as_float(s1 & 0xFFFF0000u)};
         uint32_t m[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) m[i] = some ? __float_as_uint(fmaf(f[i], inv, 12583040.f)) : 0x80u;
-        qh[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0051), __byte_perm(m[2], m[3], 0x0051), 0x5410);
+        for (int i = 0; i < 4; ++i) m[i] = some ? __float_as_uint(fmaf(f[i], inv, 12582912.f)) + (0x8080u - 0x4B400000u) : 0x8080u;
+        qh[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0062), __byte_perm(m[2], m[3], 0x0062), 0x5410);
+        qm[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0051), __byte_perm(m[2], m[3], 0x0051), 0x5410) ^ 0x80808080u;
         ql[j][w] = __byte_perm(__byte_perm(m[0], m[1], 0x0040), __byte_perm(m[2], m[3], 0x0040), 0x5410) ^ 0x80808080u;
       }
   }
@@ -333,14 +338,16 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
     }
     const int8_t* tile = ring + (cur % kStages) * few_stage(D);
     // scores of 16 keys x 8 rows: lane holds keys g, g + 8, rows 2t, 2t + 1
-    int ch[4] = {0, 0, 0, 0}, cl[4] = {0, 0, 0, 0};
+    int ch[4] = {0, 0, 0, 0}, cm[4] = {0, 0, 0, 0}, cl[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < KBLK; ++j) {
       const uint4 x0 = *reinterpret_cast<const uint4*>(tile + g * D + 64 * j + 16 * t);
       const uint4 x1 = *reinterpret_cast<const uint4*>(tile + (g + 8) * D + 64 * j + 16 * t);
       mma_s8(ch, x0.x, x1.x, x0.y, x1.y, qh[j][0], qh[j][1]);
+      mma_s8(cm, x0.x, x1.x, x0.y, x1.y, qm[j][0], qm[j][1]);
       mma_s8(cl, x0.x, x1.x, x0.y, x1.y, ql[j][0], ql[j][1]);
       mma_s8(ch, x0.z, x1.z, x0.w, x1.w, qh[j][2], qh[j][3]);
+      mma_s8(cm, x0.z, x1.z, x0.w, x1.w, qm[j][2], qm[j][3]);
       mma_s8(cl, x0.z, x1.z, x0.w, x1.w, ql[j][2], ql[j][3]);
     }
     const float lv_l = __log2f(sc);  // (of the V scales, lanes 16-31; 0, with codes 0, gives -inf)
@@ -350,9 +357,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       ks[i] = __shfl_sync(0xFFFFFFFFu, sc, g + 8 * i);
       lv[i] = __shfl_sync(0xFFFFFFFFu, lv_l, 16 + g + 8 * i);
     }
-    float c[4];  // (|256 hi + lo| < 2^31: 127 * 127 * 256 * 257)
+    float c[4];  // (|hi| <= 64: |256 hi + mid| sums stay below 2^30)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = (float)(ch[i] * 256 + cl[i]) * qs[i & 1];
+    for (int i = 0; i < 4; ++i) c[i] = fmaf((float)(ch[i] * 256 + cm[i]), 256.f, (float)cl[i]) * qs[i & 1];
     const int ka = at + g, kc = ka + 8;
     const bool in[4] = {ka < min(lim[0], key1), ka < min(lim[1], key1), kc < min(lim[0], key1), kc < min(lim[1], key1)};
     float x[4];  // masked places: -inf, whatever their scale is

@@ -434,11 +434,12 @@ pae_status pae_kv8_read(const pae_kv8* cache, void* k, void* v, const long long*
  * that may overlap; its contents carry nothing from call to call.
  * PAE_ERR_UNSUPPORTED: n_seq * n_kv_heads > 65535, n_q times the query heads
  * of a KV head > 2^22.
- * Precision: scores are fp32; a probability times its value's scale is rounded
- * to fp16 in units of the row's largest one (cached keys: by 2^-11 of itself or
- * 2^-28 of the largest, whichever is more, and by 2^-11 of the largest for a
- * whole tail of keys too small for their own 11 bits) or to bf16 (fresh keys),
- * sums are fp32. */
+ * Precision: scores are fp32 (query elements below 2^-14 of their row's largest
+ * may be rounded by 2^-22 of it); a probability times its value's scale is
+ * rounded to fp16 in units of the row's largest one (cached keys: by 2^-11 of
+ * itself or 2^-28 of the largest, whichever is more, and by 2^-11 of the largest
+ * for a whole tail of keys too small for their own 11 bits) or to bf16 (fresh
+ * keys), sums are fp32. */
 typedef struct {
   const int* lens;
   const void* q;

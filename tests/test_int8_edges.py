@@ -91,3 +91,37 @@ def test_a_long_tail_of_small_weights(nq, cap, below):
     # (assert_attention's bound with the fp16 rounding of a probability, not bf16's)
     tol = value * (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) + abs(want) * 2.0 ** -8
     assert float((got - want).abs().max()) <= tol, (float(got.min()), float(got.max()), want)
+
+
+# ------------------------------------------------------------ query precision
+@pytest.mark.gpu
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("size", [30.0, 1000.0])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_of_wide_range(d, size, nq):
+    """One channel of a query is far above the others and its key codes are zero:
+    the others decide.  Two keys with values +-1 share the weight, so an error
+    of a score shows undivided.
+
+    A probability rounds to fp16 (2^-11).  The query counts as a 24-bit integer of
+    its row's range: a channel is off by at most 2^-22 of the power of two below
+    the row's largest, which moves a score by at most 2^-22 size sum|k| scale and
+    a probability by as much (two keys: a quarter of the sum of both).  fp32
+    scores and exp2: their sums over |q k| up to about 40 are off by less than 2^-12."""
+    B, group = 8, 8
+    g = torch.Generator().manual_seed(nq + d)
+    c = fm.KvCacheInt8(B, 1, 2, d)
+    kc = torch.randint(-127, 128, (B, 1, 2, d), generator=g, dtype=torch.int8)
+    kc[..., 0] = 0
+    vc = torch.full((B, 1, 2, d), 127, dtype=torch.int8)
+    vc[:, :, 1] = -127
+    k, v = _put(c, kc, torch.full((B, 1, 2), 2.0 / 127), vc, torch.full((B, 1, 2), 1.0 / 127))
+    q = torch.randn(B, nq, group, d, generator=g)
+    q[..., 0] = size
+    q = q.to(torch.bfloat16)
+    o, a = attention_ref(q.double(), k, v, [2] * B, False, None, None, d ** -0.5)
+    got = c.attend(q.cuda(), _lens(*[2] * B))
+    score = 2.0 ** -22 * size * float(k.abs().sum(-1).max()) * d ** -0.5
+    tol = a * (2.0 ** -11 + 2.0 ** -12 + score) + o.abs() * 2.0 ** -8
+    over = ((got.cpu().double() - o).abs() - tol).max()
+    assert over <= 0, f"beyond the bound by {over:.3e}"
