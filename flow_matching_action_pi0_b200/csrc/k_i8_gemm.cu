@@ -90,6 +90,14 @@ __host__ __device__ inline I8Smem i8_layout(const I8GemmPlan& p) {
   return L;
 }
 
+// Results are (sum sx) sw: in this order a product of the scales alone, which may
+// be subnormal, does not occur.  A sum times a token scale above 2^64 could overflow
+// where the result does not: such a scale is split into x y, y = 2^64, and the
+// result is (sum x) sw y.  Both steps with y are exact.
+__device__ __forceinline__ float2 token_scale(float sx) {
+  return fabsf(sx) > 0x1p64f ? make_float2(sx * 0x1p-64f, 0x1p64f) : make_float2(sx, 1.f);
+}
+
 template <typename TO>
 __device__ __forceinline__ void st_out(TO* p, float v);
 template <>
@@ -389,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = (tm * CG + rank) * 128, t = row0 + row, f0 = tn * p.tn;
       float* sw = s_sw + buf * 256;
       for (int i = et; i < p.tn; i += kEpiWarps * 32) sw[i] = f0 + i < a.n ? __ldg(a.sw + f0 + i) : 0.f;
-      const float sx = t < a.tokens ? a.sx[t] : 0.f;
+      const float2 sx = token_scale(t < a.tokens ? a.sx[t] : 0.f);
       // the column scales are in place for all warps, and all go on or stop
       const bool got = mbar_wait(&acc_full[buf], (n >> 1) & 1, a.err.wait_ns);
       if (!bar_and_epi(1, got && s_flag[0] == 0)) {
@@ -415,15 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < NB; ++i) {
           const int c = b0 + i;
           if (c >= nc) break;
-          // (sum sx) sw, as for few tokens: a product of the scales alone may be subnormal
           float o[16];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 w = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * q);
-            o[4 * q] = (float)acc[i][4 * q] * sx * w.x;
-            o[4 * q + 1] = (float)acc[i][4 * q + 1] * sx * w.y;
-            o[4 * q + 2] = (float)acc[i][4 * q + 2] * sx * w.z;
-            o[4 * q + 3] = (float)acc[i][4 * q + 3] * sx * w.w;
+            o[4 * q] = (float)acc[i][4 * q] * sx.x * w.x * sx.y;
+            o[4 * q + 1] = (float)acc[i][4 * q + 1] * sx.x * w.y * sx.y;
+            o[4 * q + 2] = (float)acc[i][4 * q + 2] * sx.x * w.z * sx.y;
+            o[4 * q + 3] = (float)acc[i][4 * q + 3] * sx.x * w.w * sx.y;
           }
           if (!staged) {
             if (t < a.tokens && f0 + c * 16 < a.n) store16(y + (size_t)t * a.ldy + f0 + c * 16, o, a.n - (f0 + c * 16), vec);
@@ -507,7 +514,7 @@ __global__ void __launch_bounds__(256, 1)
   uint64_t* acc_full = empty + p.stages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile int* s_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* s_sx = reinterpret_cast<float*>(smem + L.sw_off);
+  float2* s_sx = reinterpret_cast<float2*>(smem + L.sw_off);  // [tn <= 64]
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int f0 = blockIdx.x * p.th, split = blockIdx.y, t0 = blockIdx.z * p.tn;
   const int nkb_all = (a.k + KB - 1) / KB;
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(256, 1)
   const bool acc_ok = mbar_wait(acc_full, 0, kDrainNs);
   if (!acc_ok) set_error(a.err, DEV_DRAIN);
   tc_fence_after();
-  for (int i = threadIdx.x; i < p.tn; i += 256) s_sx[i] = t0 + i < a.tokens ? a.sx[t0 + i] : 0.f;
+  for (int i = threadIdx.x; i < p.tn; i += 256) s_sx[i] = token_scale(t0 + i < a.tokens ? a.sx[t0 + i] : 0.f);
   const bool ok = __syncthreads_and(acc_ok ? 1 : 0) != 0 && s_flag[0] == 0;
 
   // warp w: TMEM lanes 32 (w % 4).. (features), 16-token chunks c with c % 2 == w / 4
@@ -622,8 +629,10 @@ __global__ void __launch_bounds__(256, 1)
         if (f < a.n) {
 #pragma unroll
           for (int j = 0; j < 16; ++j)
-            if (c * 16 + j < ntok)
-              st_out(y + (size_t)(t0 + c * 16 + j) * a.ldy + f, (float)v[j] * s_sx[c * 16 + j] * sw);
+            if (c * 16 + j < ntok) {
+              const float2 sx = s_sx[c * 16 + j];
+              st_out(y + (size_t)(t0 + c * 16 + j) * a.ldy + f, (float)v[j] * sx.x * sw * sx.y);
+            }
         }
       }
   } else {
@@ -661,10 +670,11 @@ __global__ void __launch_bounds__(256, 1)
           }
         const int f = f0 + r;
         const int s4[4] = {(int)sum.x, (int)sum.y, (int)sum.z, (int)sum.w};
+        const float2 sx = s_sx[tok];
         TO* yp = y + (size_t)(t0 + tok) * a.ldy + f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (f + i < a.n) st_out(yp + i, (float)s4[i] * s_sx[tok] * a.sw[f + i]);
+          if (f + i < a.n) st_out(yp + i, (float)s4[i] * sx.x * a.sw[f + i] * sx.y);
       }
     }
     cluster_sync();  // no rank leaves while another still reads its partials

@@ -125,3 +125,18 @@ def test_queries_of_wide_range(d, size, nq):
     tol = a * (2.0 ** -11 + 2.0 ** -12 + score) + o.abs() * 2.0 ** -8
     over = ((got.cpu().double() - o).abs() - tol).max()
     assert over <= 0, f"beyond the bound by {over:.3e}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens", [3, 200, 600])
+@pytest.mark.parametrize("sx,sw", [(1.37 * 2.0 ** 110, 1.61 * 2.0 ** -40), (1.61 * 2.0 ** -40, 1.37 * 2.0 ** 110)])
+def test_linear_i8_large_scales(tokens, sx, sw):
+    """A sum times the larger scale alone is past fp32 (2^22 2^110), the result
+    is not.  Two roundings of 2^-24 as for the small scales."""
+    k, n = 512, 300
+    g = torch.Generator().manual_seed(tokens)
+    x, w = torch.randint(100, 128, (tokens, k), generator=g), torch.randint(100, 128, (n, k), generator=g)
+    xs, ws = torch.full((tokens,), sx), torch.full((n,), sw)
+    want = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    got = fm.linear_i8(x.to(torch.int8).cuda(), xs.cuda(), w.to(torch.int8).cuda(), ws.cuda(), out_dtype=torch.float32)
+    assert bool(((got.cpu().double() - want).abs() <= want * (2.0 ** -23 + 2.0 ** -46)).all())
