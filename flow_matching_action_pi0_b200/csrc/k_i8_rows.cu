@@ -246,13 +246,27 @@ __global__ void __launch_bounds__(256) k_quantize_rows_any(const T* __restrict__
   const float inv = inv_scale(s);
   const float unit = rms_unit(s, inv);
   int8_t* cr = codes + (size_t)row * width;
-  float ss = 0.f;
+  // Squares in chains of 64, 256 of those, and those: equal elements round the
+  // same way every time, and one chain over a row of 2^22 was off by 2^-14.
+  // (1600 rows of 28672: 82.7 us, 78.7 with one chain.)
+  float ss = 0.f, mid = 0.f, low = 0.f;
+  int left = 64, groups = 256;
   for (int i = threadIdx.x; i < width; i += 256) {
     const float f = ld_act<T>(xr + i);
     cr[i] = inv > 0.f ? (int8_t)quant1(f, s, inv) : (int8_t)0;
-    ss = fmaf(f * unit, f * unit, ss);
+    low = fmaf(f * unit, f * unit, low);
+    if (--left == 0) {
+      mid += low;
+      low = 0.f;
+      left = 64;
+      if (--groups == 0) {
+        ss += mid;
+        mid = 0.f;
+        groups = 256;
+      }
+    }
   }
-  ss = warp_sum(ss);
+  ss = warp_sum(ss + mid + low);
   if ((threadIdx.x & 31) == 0) s_sum[threadIdx.x >> 5] = ss;
   __syncthreads();
   ss = 0.f;

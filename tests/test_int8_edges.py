@@ -140,3 +140,18 @@ def test_linear_i8_large_scales(tokens, sx, sw):
     want = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
     got = fm.linear_i8(x.to(torch.int8).cuda(), xs.cuda(), w.to(torch.int8).cuda(), ws.cuda(), out_dtype=torch.float32)
     assert bool(((got.cpu().double() - want).abs() <= want * (2.0 ** -23 + 2.0 ** -46)).all())
+
+
+# -------------------------------------------------------------------- wide rows
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [1 << 22, (1 << 22) + 3])
+def test_norms_of_very_wide_rows(width, dtype):
+    """Equal elements, whose squares round the same way every time they are
+    added: 2^14 per thread.  Groups of 64 sums, and their sums: under 400
+    roundings of 2^-24, halved by the root, and those of the scale's formula."""
+    x = torch.full((2, width), 0.1, dtype=DT[dtype], device="cuda")
+    x[1] = torch.linspace(-1, 1, width, device="cuda").to(DT[dtype])
+    _, s = fm.quantize_rows(x, rms_eps=1e-6)
+    want = (x.double().abs().amax(-1) / 127).float().double() / torch.sqrt((x.double() ** 2).mean(-1) + 1e-6)
+    assert bool(((s.double() - want).abs() <= want * 2.0 ** -16).all())
