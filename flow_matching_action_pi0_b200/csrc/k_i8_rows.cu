@@ -144,11 +144,13 @@ __device__ __forceinline__ uint2 quant8(const float* f, float s, float inv) {
                     __byte_perm(__byte_perm(m[4], m[5], 0x0040), __byte_perm(m[6], m[7], 0x0040), 0x5410));
 }
 
-// s / sqrt(mean x^2 + eps).  Squares of rows with s >= 1 are taken in units of
-// s (they cannot overflow), others as they are (eps / s^2 cannot).
-__device__ __forceinline__ float rms_unit(float s, float inv) { return s >= 1.f ? inv : 1.f; }
+// s / sqrt(mean x^2 + eps) from the mean square of x / s, which neither overflows
+// nor underflows: 1 / sqrt(mean + eps / s^2).  Where eps / s^2 leaves fp32, the
+// mean (at most 127^2) is nothing beside it.
 __device__ __forceinline__ float rms_scale(float s, float inv, float mean_sq, float eps) {
-  return s >= 1.f ? rsqrtf(mean_sq + eps * inv * inv) : s * rsqrtf(mean_sq + eps);
+  if (!(s > 0.f)) return s;  // a row of zeros, or NaN
+  const float t = eps * inv * inv;
+  return t < 0x1p100f ? rsqrtf(mean_sq + t) : s * rsqrtf(eps);
 }
 
 // ------------------------------------------------------------ row quantiser
@@ -191,7 +193,6 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
   }
   const float s = row_scale(am);
   const float inv = inv_scale(s);
-  const float unit = rms_unit(s, inv);
   int8_t* cr = codes + (size_t)row * width;
   float2 ss2 = make_float2(0.f, 0.f);
 #pragma unroll
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const T* __restrict__ x, 
       if (rms_eps > 0.f) {
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const float2 t = mul2(make_float2(f[j], f[j + 1]), make_float2(unit, unit));
+          const float2 t = mul2(make_float2(f[j], f[j + 1]), make_float2(inv, inv));
           ss2 = fma2(t, t, ss2);
         }
       }
@@ -244,7 +245,6 @@ __global__ void __launch_bounds__(256) k_quantize_rows_any(const T* __restrict__
   for (int w = 0; w < 8; ++w) am = max(am, s_max[w]);
   const float s = row_scale(am);
   const float inv = inv_scale(s);
-  const float unit = rms_unit(s, inv);
   int8_t* cr = codes + (size_t)row * width;
   // Squares in chains of 64, 256 of those, and those: equal elements round the
   // same way every time, and one chain over a row of 2^22 was off by 2^-14.
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows_any(const T* __restrict__
   for (int i = threadIdx.x; i < width; i += 256) {
     const float f = ld_act<T>(xr + i);
     cr[i] = inv > 0.f ? (int8_t)quant1(f, s, inv) : (int8_t)0;
-    low = fmaf(f * unit, f * unit, low);
+    low = fmaf(f * inv, f * inv, low);
     if (--left == 0) {
       mid += low;
       low = 0.f;

@@ -155,3 +155,21 @@ def test_norms_of_very_wide_rows(width, dtype):
     _, s = fm.quantize_rows(x, rms_eps=1e-6)
     want = (x.double().abs().amax(-1) / 127).float().double() / torch.sqrt((x.double() ** 2).mean(-1) + 1e-6)
     assert bool(((s.double() - want).abs() <= want * 2.0 ** -16).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("width", [512, 100])
+@pytest.mark.parametrize("eps", [1e-44, 1e-40, 1e-30, 1e-6, 1e20])
+def test_norms_of_small_and_large_rows(width, dtype, eps):
+    """Rows whose squares are below fp32 or above it, with an eps on either side.
+    (The bound is test_quantize_rows'; a result below 2^-126 rounds to a step of
+    2^-149, half of which is 2^-150.)"""
+    g = torch.Generator().manual_seed(width)
+    x = torch.randn(12, width, generator=g).double()
+    for i, e in enumerate((-100, -80, -74, -70, -66, -50, -1, 0, 30, 60, 90, 120)):
+        x[i] *= 2.0 ** e
+    x = x.to(DT[dtype])
+    _, s = fm.quantize_rows(x.cuda(), rms_eps=eps)
+    want = quant_ref(x.double().numpy())[1].astype(np.float64) / np.sqrt((x.double().numpy() ** 2).mean(-1) + float(np.float32(eps)))
+    assert np.all(np.abs(s.cpu().numpy() - want) <= want * 2.0 ** -17 + 2.0 ** -150)
