@@ -47,7 +47,10 @@ pae_status fail(pae_status st, const char* fmt, ...) {
   return st;
 }
 
+// (An error that is reported is also taken from the runtime, or it would fail
+// every later call as one that is still pending.)
 pae_status cuda_fail(const char* what, cudaError_t e) {
+  cudaGetLastError();
   return fail(PAE_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
@@ -61,13 +64,10 @@ pae_status check_word(const DeviceState* d, const char* fn) {
 // The current device's state, set up on first use.  Setting up allocates
 // host-mapped memory, which a stream capture does not allow.
 pae_status device_state(const char* fn, pae_stream stream, bool check_stream, DeviceState** out) {
-  cudaError_t e = cudaPeekAtLastError();
+  cudaError_t e = cudaGetLastError();  // (reported once; one that the context does not survive comes back)
   if (e != cudaSuccess) return fail(PAE_ERR_CUDA, "%s: a CUDA error from earlier work is pending (%s)", fn, cudaGetErrorString(e));
   int dev = 0;
-  if ((e = cudaGetDevice(&dev)) != cudaSuccess) {
-    cudaGetLastError();
-    return cuda_fail("cudaGetDevice", e);
-  }
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return cuda_fail("cudaGetDevice", e);
   if (dev < 0 || dev >= kMaxDevices) return fail(PAE_ERR_UNSUPPORTED, "%s: device ordinals of 64 and above are not supported", fn);
   std::lock_guard<std::mutex> lock(g_mu);
   DeviceState& d = g_dev[dev];
@@ -90,10 +90,7 @@ pae_status device_state(const char* fn, pae_stream stream, bool check_stream, De
       *d.err_host = 0;
       e = cudaHostGetDevicePointer(reinterpret_cast<void**>(&d.err_dev), d.err_host, 0);
     }
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return cuda_fail(fn, e);
-    }
+    if (e != cudaSuccess) return cuda_fail(fn, e);
     d.encode = reinterpret_cast<EncodeTiledFn>(enc);
     d.ready = true;
   }
@@ -203,6 +200,7 @@ pae_status pae_int8_sync(pae_stream stream) {
 }
 
 void pae_int8_clear_error(void) {
+  cudaGetLastError();  // one left pending
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
     cudaGetLastError();
@@ -210,7 +208,7 @@ void pae_int8_clear_error(void) {
   }
   std::lock_guard<std::mutex> lock(g_mu);
   if (!g_dev[dev].err_host) return;
-  cudaDeviceSynchronize();
+  if (cudaDeviceSynchronize() != cudaSuccess) cudaGetLastError();
   if (*(volatile int*)g_dev[dev].err_host != DEV_DRAIN) *(volatile int*)g_dev[dev].err_host = 0;
 }
 

@@ -361,11 +361,13 @@ pae_status pae_precompute_tables_static(int layers, int width, int dtype, const 
  * pae_last_error(NULL).  A device-side bounded wait that runs out (2 s) makes
  * the next of these calls on the device, or pae_int8_sync, return
  * PAE_ERR_TIMEOUT until pae_int8_clear_error; after a failed drain (the
- * message says so) the error stays.  The first call on a device sets up the
- * kernels and an error word in host memory and cannot be captured into a
- * graph (PAE_ERR_STATE); pae_int8_init does it ahead.  Later calls can be
- * captured.  Calls on different streams may overlap, apart from sharing a
- * workspace, a cache position or an output.  Results are bitwise reproducible.
+ * message says so) the error stays.  An error that earlier work of the thread
+ * left in the CUDA runtime is reported once, by the next of these calls, which
+ * then does nothing else.  The first call on a device sets up the kernels and
+ * an error word in host memory and cannot be captured into a graph
+ * (PAE_ERR_STATE); pae_int8_init does it ahead.  Later calls can be captured.
+ * Calls on different streams may overlap, apart from sharing a workspace, a
+ * cache position or an output.  Results are bitwise reproducible.
  *
  * A row x in 8 bits: scale s = max|x| / 127 rounded to fp32 (0 if below
  * 2^-120: the row is stored as zeros), codes rint(x_i / s) of the exact
