@@ -49,6 +49,7 @@ cudaError_t launch_quantize_rows(bool in_bf16, const void* x, long long ldx, int
 
 // ------------------------------------------------------------- int8 product
 // y[t][f] = (sum_k x[t][k] w[f][k]) sx[t] sw[f], int32 sums.
+constexpr int kMaxI8K = 131056;  // the last multiple of 16 at which 2^14 k stays below 2^31
 struct I8GemmPlan {
   int cg;       // CTAs per tile (2: pairs of cta_group::2; not with swap)
   int swap;     // 1: weight rows on the MMA's M side, tokens on its N side

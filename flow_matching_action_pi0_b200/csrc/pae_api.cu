@@ -1183,6 +1183,8 @@ pae_status validate_config(const pae_config* c) {
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: the 8-bit prefix needs PAE_BF16 or PAE_W4A16");
   if ((flags & PAE_PREFIX_W8A8) && (!(flags & PAE_KV_INT8) || c->prefix_width <= 0))
     return fail(nullptr, PAE_ERR_ARG, "config: PAE_PREFIX_W8A8 needs PAE_KV_INT8 and prefix_width > 0");
+  if ((flags & PAE_PREFIX_W8A8) && c->prefix_width > kMaxI8K)
+    return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: PAE_PREFIX_W8A8 needs prefix_width <= %d (32-bit sums)", kMaxI8K);
   if (flags && (long long)c->max_batch * c->n_kv_heads > 65535)
     return fail(nullptr, PAE_ERR_UNSUPPORTED, "config: the 8-bit prefix needs max_batch * n_kv_heads <= 65535");
   if (c->n_q_heads % c->n_kv_heads != 0)

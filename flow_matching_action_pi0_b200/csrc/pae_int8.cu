@@ -236,7 +236,7 @@ pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signe
   const char* fn = "pae_linear_i8";
   if (!known(dtype)) return fail(PAE_ERR_ARG, "%s: dtype must be PAE_FP32 or PAE_BF16", fn);
   if (tokens < 0 || n < 1 || k < 1) return fail(PAE_ERR_ARG, "%s: tokens must be >= 0, n and k >= 1", fn);
-  if (k % 16 || k > 131056) return fail(PAE_ERR_UNSUPPORTED, "%s: k must be a multiple of 16 and at most 131056 (32-bit sums)", fn);
+  if (k % 16 || k > kMaxI8K) return fail(PAE_ERR_UNSUPPORTED, "%s: k must be a multiple of 16 and at most %d (32-bit sums)", fn, kMaxI8K);
   if (tokens > (1 << 24) || n > (1 << 24)) return fail(PAE_ERR_UNSUPPORTED, "%s: tokens and n must be at most 2^24", fn);
   if (tokens == 0) return PAE_OK;
   if (!x || !x_scale || !w || !w_scale || !y) return fail(PAE_ERR_ARG, "%s: a pointer argument is NULL", fn);

@@ -64,7 +64,7 @@ typedef enum {
  *   the bytes of the bf16 slots; every Euler step attends over them and the
  *   action tokens' own bf16 keys.  K/V rows given to pae_set_prefix must start
  *   on 16 bytes.  PAE_OPT_PERSISTENT and PAE_OPT_DATAFLOW run the graph.
- * PAE_PREFIX_W8A8 (with PAE_KV_INT8 and prefix_width > 0):
+ * PAE_PREFIX_W8A8 (with PAE_KV_INT8 and prefix_width in [1, 131056]):
  *   pae_set_prefix_hidden projects in 8-bit integers; w_prefix_kv is quantised
  *   at pae_create with one scale per output row, the normalised hidden states
  *   with one per token. */

@@ -16,6 +16,7 @@ import torch
 
 import flow_matching_action_pi0_b200 as fm
 from flow_matching_action_pi0_b200 import build as fbuild
+from tests.test_abi import _cfg, _create_status
 from tests.test_int8_ops import DT, HALF_ULP, assert_attention, attention_ref, quant_ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -212,3 +213,14 @@ def test_a_refused_call_leaves_the_operators_usable():
     r = subprocess.run([sys.executable, "-c", PENDING], capture_output=True, text=True, timeout=300, cwd=ROOT)
     assert r.returncode == 0 and "usable" in r.stdout, r.stderr[-2000:]
 
+
+
+# -------------------------------------------------------------------- contexts
+def test_a_prefix_too_wide_for_32_bit_sums_is_refused():
+    def create(width):
+        return _create_status(_cfg(kv_int8=True, prefix_w8a8=True, prefix_width=width))[::2]
+
+    st, msg = create(131072)  # the next multiple of 64 past the product's 131056
+    assert st == fm.PAE_ERR_UNSUPPORTED and "prefix_width" in msg
+    st, msg = create(131008)  # the last one within: the next check is reached, the missing weights
+    assert st == fm.PAE_ERR_ARG and "NULL" in msg
