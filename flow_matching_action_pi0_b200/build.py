@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -53,21 +54,70 @@ def _tensors_command():
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(TENSORS):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(TENSORS))
-    deps = sources() + [_TENSORS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h"))
-    return any(os.path.getmtime(p) > t for p in deps)
+def _newer(target: str, deps) -> bool:
+    """`target` is there and no file of `deps` is newer."""
+    if not os.path.exists(target):
+        return False
+    t = os.path.getmtime(target)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def _torch_version():
+    """The installed PyTorch, None without one (looked up without importing it)."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+
+
+def _lib_current() -> bool:
+    return _newer(LIB, sources() + [p for pat in ("*.cuh", "*.h") for p in glob.glob(os.path.join(CSRC, pat))] +
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _tensors_current() -> bool:
+    stamp = _stamp()
+    if not _newer(TENSORS, [_TENSORS_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))) or not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == _torch_version()
+
+
+def _stamp() -> str:
+    """The file that says which PyTorch the tensor module was built against."""
+    return os.path.join(HERE, "_build", os.path.basename(TENSORS) + ".torch")
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
-    tensors = subprocess.Popen(_tensors_command(), stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    """libpae.so first, which needs nvcc alone, then the tensor module where
+    PyTorch is installed; a tensor module that does not compile is an error, but
+    leaves libpae.so in place."""
+    os.makedirs(os.path.join(HERE, "_build"), exist_ok=True)
+    if force or not _lib_current():
+        _build_lib(verbose, ptxas_v)
+    version = _torch_version()
+    if version is None:
+        print(f"PyTorch is not installed: {os.path.basename(TENSORS)} is left out, int8.py needs it")
+    elif force or not _tensors_current():
+        _build_tensors(version, verbose)
+    return LIB
+
+
+def _build_tensors(version: str, verbose: bool) -> None:
+    cmd = _tensors_command()
+    if verbose:
+        print(" ".join(cmd))
+    p = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if p.returncode:
+        sys.stdout.write(p.stdout)
+        raise RuntimeError(f"compilation failed for: {_TENSORS_SRC} ({LIB} is built)")
+    os.replace(TENSORS + ".tmp", TENSORS)
+    with open(_stamp(), "w") as f:
+        f.write(version)
+
+
+def _build_lib(verbose: bool, ptxas_v: bool) -> None:
     objdir = os.path.join(HERE, "_build")
-    os.makedirs(objdir, exist_ok=True)
     flags = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
                     "-I", INCLUDE, "-I", CSRC]
     if ptxas_v:
@@ -88,21 +138,15 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             sys.stdout.write(out)
         if p.returncode:
             failed.append(src)
-    out, _ = tensors.communicate()
-    if tensors.returncode:
-        sys.stdout.write(out)
-        failed.append(_TENSORS_SRC)
     if failed:
-        raise RuntimeError("compilation failed for: " + ", ".join(failed))
+        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
     tmp = LIB + ".tmp"
     cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", tmp] + objs + ["-lcudart_static", "-ldl",
                                                                                       "-lpthread", "-lrt"]
     if verbose:
         print(" ".join(cmd))
     subprocess.run(cmd, check=True)
-    os.replace(TENSORS + ".tmp", TENSORS)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -21,7 +21,8 @@ def _bind():
     try:
         from flow_matching_action_pi0_b200 import _int8_tensors as ops
     except ImportError as e:
-        raise RuntimeError(f"{_build.TENSORS} is not built; run `python -m flow_matching_action_pi0_b200.build`") from e
+        raise RuntimeError(f"{_build.TENSORS} is not built, or not against this PyTorch ({e}); "
+                           "run `python -m flow_matching_action_pi0_b200.build`") from e
     lib = _fm.lib()
     names = ("pae_quantize_rows", "pae_linear_i8", "pae_kv8_write", "pae_kv8_read", "pae_kv8_attention")
     ops.bind(tuple(ctypes.cast(lib[name], ctypes.c_void_p).value for name in names), _fm._check)

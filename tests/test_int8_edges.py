@@ -5,6 +5,7 @@ rows, products of several tiles per SM, errors that were left pending.
 Tolerances count roundings: one to a type t is off by at most eps(t) / 2 relative
 to the value (bf16 2^-8, fp16 2^-11, fp32 2^-24).
 """
+import ctypes
 import math
 import os
 import subprocess
@@ -224,3 +225,48 @@ def test_a_prefix_too_wide_for_32_bit_sums_is_refused():
     assert st == fm.PAE_ERR_UNSUPPORTED and "prefix_width" in msg
     st, msg = create(131008)  # the last one within: the next check is reached, the missing weights
     assert st == fm.PAE_ERR_ARG and "NULL" in msg
+
+
+# ----------------------------------------------------------------------- build
+@pytest.fixture
+def small_tree(tmp_path, monkeypatch):
+    """The build on one small source in a folder of its own."""
+    (tmp_path / "csrc").mkdir()
+    (tmp_path / "csrc" / "one.cu").write_text('extern "C" int pae_one(void) { return 1; }\n')
+    (tmp_path / "csrc" / "int8_tensors.cpp").write_text("this is not C++\n")
+    for name, path in dict(HERE=".", CSRC="csrc", LIB="libpae.so", TENSORS="_int8_tensors.so",
+                           _TENSORS_SRC="csrc/int8_tensors.cpp").items():
+        monkeypatch.setattr(fbuild, name, str(tmp_path / path))
+    return tmp_path
+
+
+def test_the_library_builds_without_pytorch(small_tree, monkeypatch):
+    def nothing():
+        raise AssertionError("the tensor module was compiled")
+
+    monkeypatch.setattr(fbuild, "_torch_version", lambda: None)
+    monkeypatch.setattr(fbuild, "_tensors_command", nothing)
+    assert fbuild.build() == fbuild.LIB
+    assert ctypes.CDLL(fbuild.LIB).pae_one() == 1
+
+
+def test_a_tensor_module_that_fails_leaves_the_library(small_tree, capsys):
+    with pytest.raises(RuntimeError, match="int8_tensors"):
+        fbuild.build()
+    assert ctypes.CDLL(fbuild.LIB).pae_one() == 1
+    assert not os.path.exists(fbuild.TENSORS)
+
+
+def test_a_tensor_module_for_another_pytorch_is_built_again(small_tree, monkeypatch):
+    (small_tree / "csrc" / "int8_tensors.cpp").write_text('extern "C" int two(void) { return 2; }\n')
+    built = []
+
+    def command():
+        built.append(1)
+        return ["g++", "-shared", "-fPIC", fbuild._TENSORS_SRC, "-o", fbuild.TENSORS + ".tmp"]
+
+    monkeypatch.setattr(fbuild, "_tensors_command", command)
+    for version, times in (("1.0", 1), ("1.0", 1), ("1.1", 2), ("1.1", 2)):
+        monkeypatch.setattr(fbuild, "_torch_version", lambda v=version: v)
+        fbuild.build()
+        assert len(built) == times
