@@ -59,14 +59,22 @@ class Kv8Plan:
 
 class KvCacheInt8:
     """An int8 K/V cache: codes k, v [n_slots, n_kv_heads, capacity, head_dim]
-    and scales k_scale, v_scale [n_slots, n_kv_heads, capacity]."""
+    and scales k_scale, v_scale [n_slots, n_kv_heads, capacity].  The tensors may
+    be filled in place; they stay the cache's own."""
+
+    # the calls take the addresses that were found once: another tensor in the
+    # place of one of these would leave them in freed memory
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    k_scale = property(lambda self: self._k_scale)
+    v_scale = property(lambda self: self._v_scale)
 
     def __init__(self, n_slots: int, n_kv_heads: int, capacity: int, head_dim: int, device="cuda"):
         shape = (n_slots, n_kv_heads, capacity, head_dim)
-        self.k = torch.zeros(shape, dtype=torch.int8, device=device)
-        self.v = torch.zeros(shape, dtype=torch.int8, device=device)
-        self.k_scale = torch.zeros(shape[:3], dtype=torch.float32, device=device)
-        self.v_scale = torch.zeros(shape[:3], dtype=torch.float32, device=device)
+        self._k = torch.zeros(shape, dtype=torch.int8, device=device)
+        self._v = torch.zeros(shape, dtype=torch.int8, device=device)
+        self._k_scale = torch.zeros(shape[:3], dtype=torch.float32, device=device)
+        self._v_scale = torch.zeros(shape[:3], dtype=torch.float32, device=device)
         self.shape = shape
         self.device = self.k.device
         self._c = _fm.pae_kv8(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(),

@@ -270,3 +270,15 @@ def test_a_tensor_module_for_another_pytorch_is_built_again(small_tree, monkeypa
         monkeypatch.setattr(fbuild, "_torch_version", lambda v=version: v)
         fbuild.build()
         assert len(built) == times
+
+
+# ----------------------------------------------------------------------- cache
+def test_the_tensors_of_a_cache_cannot_be_exchanged():
+    """The cache's calls hold their addresses."""
+    c = fm.KvCacheInt8(1, 1, 8, 64, device="cpu")
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name).clone())
+        getattr(c, name).fill_(1)
+        assert bool((getattr(c, name) == 1).all())
+    assert c.shape == (1, 1, 8, 64) and c.k.shape == c.shape
