@@ -144,6 +144,39 @@ def test_linear_i8_large_scales(tokens, sx, sw):
     assert bool(((got.cpu().double() - want).abs() <= want * (2.0 ** -23 + 2.0 ** -46)).all())
 
 
+# -------------------------------------------------------------- int8 product
+def _product(tokens, n, k, sx=None, sw=None):
+    g = torch.Generator(device="cuda").manual_seed(tokens + 7 * n + 13 * k)
+    x = torch.randint(-128, 128, (tokens, k), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-128, 128, (n, k), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.rand(tokens, generator=g, device="cuda") + 0.01
+    ws = torch.rand(n, generator=g, device="cuda") + 0.01
+    return x, xs, w, ws
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens,n,k", [(2500, 6008, 96), (2501, 6001, 96), (3997, 10000, 1024), (3997, 9999, 1024),
+                                        (7743, 4112, 512)])
+def test_linear_i8_of_several_tiles_per_sm(tokens, n, k, out):
+    """A CTA (the first two shapes) or a pair of CTAs (the others) walks three to
+    eight tiles, the last ones ragged: accumulators, scales and output boxes in
+    turn.  Whatever the plan, tiles are at most 256 x 256 (pairs) or 128 x 256, so
+    every shape is more than three rounds over the SMs.  Rows that start on 16
+    bytes leave as tensor stores, the others along the rows."""
+    assert -(-tokens // 256) * -(-n // 256) >= 3 * 74
+    x, xs, w, ws = _product(tokens, n, k)
+    ref = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    y = fm.linear_i8(x, xs, w, ws, out_dtype=DT[out])
+    # the sum is exact; its conversion, two products and the output round
+    assert bool(((y.double() - ref).abs() <= ref.abs() * (3 * 2.0 ** -24 + HALF_ULP[out])).all())
+    big = torch.full((tokens + 2, n + 8), 7.0, dtype=DT[out], device="cuda")
+    fm.linear_i8(x, xs, w, ws, out=big[1:-1, :n])
+    assert torch.equal(big[1:-1, :n], y)
+    big[1:-1, :n] = 7.0
+    assert bool((big == 7.0).all())
+
+
 # -------------------------------------------------------------------- wide rows
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
