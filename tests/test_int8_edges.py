@@ -260,6 +260,38 @@ def test_a_prefix_too_wide_for_32_bit_sums_is_refused():
     assert st == fm.PAE_ERR_ARG and "NULL" in msg
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("opt,how", [("FUSED_NORM", 1), ("FACTORED_NORM", 2)])
+@pytest.mark.parametrize("rope", [0.0, 10000.0])
+@pytest.mark.parametrize("batch", [1, 3])
+def test_norms_in_the_projections_over_an_int8_prefix(opt, how, rope, batch):
+    """The other placements of the norm project q, k and v through epilogues of
+    their own, which put the action keys into the int8 prefix's buffer too."""
+    import oracle  # noqa: F401
+    import workloads as wl
+    from tests.helpers import assert_parity, oracle_rows, run_gpu, set_prefixes
+    from workloads import device as wd
+    cfg = wl.TINY_FP32.replace(name="kv8_norms", dtype=wl.BF16, batch=batch, rope_base=rope)
+    W = wl.make_weights(cfg)
+    ex = fm.ActionExpert(fm.make_config(kv_int8=True, **wd.abi_config(cfg)), wd.upload_weights(cfg, W))
+    try:
+        lengths = [64, 17, 0][:batch]
+        ks, vs = wl.make_prefix(cfg, lengths=lengths)
+        set_prefixes(ex, cfg, ks, vs)
+        ex.set_option(getattr(fm, "PAE_OPT_" + opt), 1)
+        assert ex.query(fm.PAE_Q_FUSED_NORM, batch) == how
+        ex.precompute_tables(wl.uniform_grid(cfg.steps))
+        noise = wl.make_noise(cfg)
+        out = run_gpu(ex, noise)
+        shp = (cfg.layers, batch, cfg.n_kv_heads, cfg.prefix)
+        vals = [np.frombuffer(ex.debug_copy(n + "codes").tobytes(), np.int8).reshape(shp + (cfg.head_dim,)).astype(np.float64) *
+                np.frombuffer(ex.debug_copy(n + "scales").tobytes(), np.float32).reshape(shp)[..., None] for n in "kv"]
+        k8, v8 = [[[t[l, b, :, :n].transpose(1, 0, 2) for l in range(cfg.layers)] for b, n in enumerate(lengths)] for t in vals]
+        assert_parity(out, oracle_rows(cfg, W, k8, v8, noise, wl.uniform_grid(cfg.steps)), cfg.dtype, cfg.name)
+    finally:
+        ex.close()
+
+
 # ----------------------------------------------------------------------- build
 @pytest.fixture
 def small_tree(tmp_path, monkeypatch):
