@@ -64,12 +64,6 @@ constexpr int kWarps = 4;
 constexpr int kTileKeys = 16;
 constexpr float kLift = 7.f, kTop = 15.f;  // log2 of the largest c where the reference is set, and where it moves
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void mma_f16(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -98,17 +92,6 @@ __device__ __forceinline__ uint32_t bytes_f16x2(uint32_t w) {
   const uint32_t u = (w & 0x00FF00FFu) ^ 0x64806480u;
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&u), __floats2half2_rn(1152.f, 1152.f));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;  // one instruction for the pair, round to nearest even
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // Units of 64 keys of a sequence: at least one, so that an empty sequence is
@@ -615,8 +598,8 @@ __global__ void __launch_bounds__(NT) k_kv8_merge_few(const Kv8AttnArgs a, int r
   }
 }
 
-// The parts of k_kv8_attn_tc: o = sum_s w_s O_s / sum_s w_s l_s with w_s =
-
+// The parts of k_kv8_attn_tc, averages over their keys and the logarithms lw_s of
+// their weights: o = sum_s 2^lw_s O_s / sum_s 2^lw_s.  rowsp: rows of a part.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int splits, int rowsp) {
   constexpr int C4 = D / 4, NR = 256 / C4;  // rows per block
@@ -667,8 +650,7 @@ cudaError_t few_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, bool pdl, cud
 template <int D>
 cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_t st) {  // (PDL behind its own attention)
   const int nr = 1024 / D;  // rows per block
-  return launch_ex(k_kv8_merge<D>, dim3((a.group * a.n_q + nr - 1) / nr, a.n_seq * a.c.heads), dim3(256), 0, st, 1, true, a, p.splits,
-                   p.qtiles * (p.tc ? 128 : 8));
+  return launch_ex(k_kv8_merge<D>, dim3((a.group * a.n_q + nr - 1) / nr, a.n_seq * a.c.heads), dim3(256), 0, st, 1, true, a, p.splits, p.qtiles * 128);
 }
 
 }  // namespace

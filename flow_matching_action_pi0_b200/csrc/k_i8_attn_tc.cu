@@ -61,16 +61,6 @@ constexpr float kLift = 3.f, kTop = 11.f;
 constexpr int kSpread = 3;                 // of a narrow chunk's value scales, see the scale warp
 constexpr long long kDrainNs = 4000000000LL;
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;  // one instruction for the pair, round to nearest even
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -92,11 +82,6 @@ __device__ __forceinline__ uint32_t biased_f16x2(uint32_t u, uint32_t sel) {
   const uint32_t w = __byte_perm(u, 0x64646464u, sel);
   const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&w), __floats2half2_rn(1152.f, 1152.f));
   return *reinterpret_cast<const uint32_t*>(&r);
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // OR over the 128 threads of the four warps that share 32 rows.
@@ -128,12 +113,6 @@ __device__ __forceinline__ bool rows_and(int id, bool v) {
   return r != 0;
 }
 
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // D[tmem] (+)= A B^T, bf16, descriptors as (low word, common high word).  The
 // accumulate flag is a compile-time constant, so an MMA costs little more than
 // its own issue.
@@ -160,9 +139,6 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
-}
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {

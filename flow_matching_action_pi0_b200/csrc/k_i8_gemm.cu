@@ -178,9 +178,6 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if ((long long)(globaltimer_ns() - t0) > limit_ns) return false;
   }
 }
-__device__ __forceinline__ void sts128(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int x, int y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(tm)),
@@ -203,13 +200,6 @@ __device__ __forceinline__ bool bar_and_epi(int id, bool v) {
   return r != 0;
 }
 
-// One lane of a converged warp (the loops below are walked by whole warps, so
-// that stage addresses and descriptors live in uniform registers).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
 // Stage and phase of a ring position, stepped without divisions (the ring
 // length is a run-time number, and both threads of the pipeline take a step
 // every few hundred cycles).
