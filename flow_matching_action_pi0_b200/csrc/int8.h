@@ -154,10 +154,13 @@ struct Kv8AttnArgs {
   int n_seq, n_q, n_new, group;  // group = query heads per KV head
   int causal;
   float scale_log2;         // softmax scale x log2(e)
-  float* part_o;            // averages over the part's keys: tc [n_seq * heads][splits][rows][d], else [blocks][2][8][d]
+  float* part_o;            // averages over the part's keys (see kPartShift): tc [n_seq * heads][splits][rows][d], else [blocks][2][8][d]
   float2* part_ml;          // their weights as (log2, 1), see part_weight
   DevErr err;
 };
+// Parts are parked as averages x 2^-kPartShift, so that the sum of up to 2^14 of them
+// cannot overflow where their average does not.
+constexpr float kPartShift = 14.f;
 // A part's weight, the log2 of its row sum, as a maximum and a sum for the
 // merge: (-inf, 0) where the row saw no key, (0, NaN) where its scores are NaN.
 __device__ __forceinline__ float2 part_weight(float lw) {

@@ -23,7 +23,7 @@
 // step: the row sum counts what they lose).  The row sums have a reference m of their own, since a key may weigh much and
 // carry little: sum p_j in fp32, lane by lane.  The two meet in the exponent of
 // the row's last factor, 2^(ref - m) / sum, and partial rows are parked as
-// averages with the logarithm of their weight, so no size of V overflows.
+// averages with the logarithm of their weight, so no size of V overflows or is lost.
 //
 // Bound: bytes of the cache (2 (d + 4) per key and KV head).  The G query
 // heads of a KV head share every byte, 8 rows at a time as the N side of
@@ -467,7 +467,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
         *reinterpret_cast<float4*>(dst + (8 * VB) * j + VB * g + 2 * m) =
             make_float4(o[j][m][i] * f, o[j][m][2 + i] * f, o[j][m + 1][i] * f, o[j][m + 1][2 + i] * f);
   }
-  // a row's last factor and the logarithm of its weight, by one warp's first lanes
+  const bool whole = u0 == 0 && u1 == units;
+  // the root of a row's last factor (2^(M - lw) may be below fp32 where the average
+  // is not) and the logarithm of its weight, by one warp's first lanes
   if (threadIdx.x < 8) {
     const int r = threadIdx.x;
     float M = -INFINITY, X = -INFINITY, l = 0.f;
@@ -479,10 +481,9 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) l += s_x[w][r] == -INFINITY ? s_l[w][r] : s_l[w][r] * ex2(s_x[w][r] - X);
     const float lw = X == -INFINITY ? l : X + __log2f(l);  // (without a maximum l is 0 or NaN)
-    s_row[r] = l == 0.f ? make_float2(0.f, -INFINITY) : make_float2(ex2(M - lw), lw);  // no visible key: zeros
+    s_row[r] = l == 0.f ? make_float2(0.f, -INFINITY) : make_float2(ex2(0.5f * (M - lw - (whole ? 0.f : kPartShift))), lw);  // no visible key: zeros
   }
   __syncthreads();
-  const bool whole = u0 == 0 && u1 == units;
 #pragma unroll
   for (int e = threadIdx.x; e < 8 * (D / 4); e += kWarps * 32) {
     const int r = e / (D / 4), c4 = e - r * (D / 4);
@@ -496,16 +497,17 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
       acc.z += x.z;
       acc.w += x.w;
     }
+    acc = make_float4(acc.x * f * f, acc.y * f * f, acc.z * f * f, acc.w * f * f);
     const int row = rg * 8 + r;
     if (whole) {
       if (row < rows) {
         const int qi = row / a.group, hl = row - qi * a.group;
         bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
-        *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * f, acc.y * f), pack_bf16(acc.z * f, acc.w * f));
+        *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
       }
     } else {
       const size_t pr = ((size_t)blockIdx.x * 2 + (u0 == 0 ? 1 : 0)) * 8 + r;
-      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+      *reinterpret_cast<float4*>(a.part_o + pr * D + 4 * c4) = acc;
       if (c4 == 0) a.part_ml[pr] = part_weight(lw);
     }
   }
@@ -518,6 +520,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 256 ? 2 : 4) k_kv8_attn_few(
   __syncthreads();           // s_o and the statistics are free again
   }
 }
+
+constexpr float kUnshift = 16384.f;  // 2^kPartShift
 
 // (m, l, acc) joined with the row x of maximum and sum ml; no maximum: nothing
 // was visible there, and x is passed over.
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(NT) k_kv8_merge_few(const Kv8AttnArgs a, int r
 #pragma unroll
     for (int s = 1; s < NS; ++s) merge_part(s_ml[s], s_acc[s * C4 + c4], m, l, acc);
     const int qi = row / a.group, hl = row - qi * a.group;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : kUnshift / l;
     bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
     *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
   }
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(256) k_kv8_merge(const Kv8AttnArgs a, int spli
   join(0);
   for (int s0 = NP; s0 < splits; s0 += NP) join(s0);
   const int qi = row / a.group, hl = row - qi * a.group;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : kUnshift / l;
   bf16* op = a.o + b * a.o_seq + qi * a.o_tok + (long long)(h * a.group + hl) * a.o_head + 4 * c4;
   *reinterpret_cast<uint2*>(op) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }

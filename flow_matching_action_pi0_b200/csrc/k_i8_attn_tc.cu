@@ -384,9 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
       const uint32_t b0 = __float_as_uint(v[0]), b1 = __float_as_uint(v[1]);
       const int hi = (int)(__reduce_max_sync(0xffffffffu, max(b0 & 0x7FFFFFFFu, b1 & 0x7FFFFFFFu)) >> 23);
       const int lo = (int)(__reduce_min_sync(0xffffffffu, min(b0, b1)) >> 23);
-      const bool narrow = hi < 255 && lo > 0 && hi - lo <= kSpread && (c0 + i) * CK < all_see;
+      const bool narrow = hi < 254 && lo > 0 && hi - lo <= kSpread && (c0 + i) * CK < all_see;
       const int e = narrow ? lo - 127 : 0;
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-E (-120 <= E <= 121)
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-E (-126 <= E <= 126)
       float* sl = s_sc + slot * kSc;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -654,7 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
     const float lw = X == -INFINITY ? l : X + __log2f(l);
     // O in units of 2^ref -> the average over the keys; no visible key, or none
     // with a value (ref is then not set, O is 0, or NaN of a NaN value scale): zeros
-    const float inv = l == 0.f || (!has && l == l) ? 0.f : ex2(ref - lw);
+    // 2^(ref - lw) may be below fp32 where the average is not: its root, twice
+    const float root = l == 0.f || (!has && l == l) ? 0.f : ex2(0.5f * (ref - lw - (splits > 1 ? kPartShift : 0.f)));
     // Output rows go through shared memory (every MMA is done: the tiles are
     // free), so that a row leaves as one run of 16-byte stores; straight from
     // the registers, a warp's store touches 32 rows and the 128 rows of a tile
@@ -675,19 +676,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv8_attn_tc(const Kv8AttnArgs a
 #pragma unroll
         for (int t = 0; t < 16; ++t) ov[t] = 0.f;
       }
+#pragma unroll
+      for (int t = 0; t < 16; ++t) ov[t] = ov[t] * root * root;
       if (splits == 1) {
         const uint32_t ch = (uint32_t)(oc0 + j) / 8;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
-          sts128(srow + (((ch + t) ^ (r & 7)) << 4), pack_bf16(ov[8 * t] * inv, ov[8 * t + 1] * inv),
-                 pack_bf16(ov[8 * t + 2] * inv, ov[8 * t + 3] * inv), pack_bf16(ov[8 * t + 4] * inv, ov[8 * t + 5] * inv),
-                 pack_bf16(ov[8 * t + 6] * inv, ov[8 * t + 7] * inv));
+          sts128(srow + (((ch + t) ^ (r & 7)) << 4), pack_bf16(ov[8 * t], ov[8 * t + 1]),
+                 pack_bf16(ov[8 * t + 2], ov[8 * t + 3]), pack_bf16(ov[8 * t + 4], ov[8 * t + 5]),
+                 pack_bf16(ov[8 * t + 6], ov[8 * t + 7]));
       } else {
         const uint32_t ch = (uint32_t)(oc0 + j) / 4;
 #pragma unroll
         for (int t = 0; t < 4; ++t)
-          sts128(srow + (((ch + t) ^ (r & 7)) << 4), __float_as_uint(ov[4 * t] * inv), __float_as_uint(ov[4 * t + 1] * inv),
-                 __float_as_uint(ov[4 * t + 2] * inv), __float_as_uint(ov[4 * t + 3] * inv));
+          sts128(srow + (((ch + t) ^ (r & 7)) << 4), __float_as_uint(ov[4 * t]), __float_as_uint(ov[4 * t + 1]),
+                 __float_as_uint(ov[4 * t + 2]), __float_as_uint(ov[4 * t + 3]));
       }
     }
     ok = rows_and(1 + (warp & 3), ok);

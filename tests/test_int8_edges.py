@@ -65,6 +65,26 @@ def test_values_of_zero_under_low_scores(nq, cap, zeros, causal):
     assert bool(torch.isnan(c.attend(q.cuda(), _lens(cap), causal=causal)[:, sees]).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [2.0 ** 127, 2.0 ** 126, 2.0 ** 100, 2.0 ** -100, 2.0 ** -110, 1.5 * 2.0 ** -120])
+@pytest.mark.parametrize("nq,cap,fresh", [(1, 200, 0), (1, 3000, 0), (600, 100, 0), (200, 600, 0), (3, 100, 1)])
+def test_values_at_the_ends_of_fp32(nq, cap, fresh, scale):
+    """Value scales up to 2^127 (codes up to 1: results stay finite) and down to
+    the smallest the quantiser gives; results are normal numbers throughout."""
+    d, group = 64, 4
+    g = torch.Generator().manual_seed(nq + cap)
+    c = fm.KvCacheInt8(1, 1, cap, d)
+    kc = torch.randint(-127, 128, (1, 1, cap, d), generator=g, dtype=torch.int8)
+    most = 1 if scale >= 2.0 ** 120 else 127
+    vc = torch.randint(0, most + 1, (1, 1, cap, d), generator=g, dtype=torch.int8)
+    k, v = _put(c, kc, torch.full((1, 1, cap), 1.0 / 64), vc, torch.full((1, 1, cap), scale))
+    q = torch.randn(1, nq, group, d, generator=g).to(torch.bfloat16)
+    new = [torch.zeros(1, fresh, 1, d, dtype=torch.bfloat16)] * 2 if fresh else [None, None]
+    o, a = attention_ref(q.double(), k, v, [cap], False, *[None if t is None else t.double() for t in new], d ** -0.5)
+    got = c.attend(q.cuda(), _lens(cap), k_new=new[0] if not fresh else new[0].cuda(), v_new=new[1] if not fresh else new[1].cuda())
+    assert_attention(got, o, a)
+
+
 # ------------------------------------------------------------------ long tails
 @pytest.mark.gpu
 @pytest.mark.parametrize("below", [25.4, 27.5])
