@@ -252,8 +252,11 @@ pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signe
   if ((st = make_map(d, &rows, p.swap ? w : x, p.swap ? n : tokens, k, i8_rows_box(p))) != PAE_OK) return st;
   if ((st = make_map(d, &cols, p.swap ? x : w, p.swap ? tokens : n, k, i8_cols_box(p))) != PAE_OK) return st;
   const size_t es = dtype == PAE_BF16 ? 2 : 4;
-  // whole boxes of 128 bytes per tile: a box may not reach into the next tile's columns
-  const bool tma = !p.swap && p.tn % (128 / es) == 0 && aligned(y, 16) && (size_t)ldy * es % 16 == 0 && (size_t)ldy * es < (1ULL << 40);
+  // Whole boxes of 128 bytes per tile: a box may not reach into the next tile's
+  // columns.  Whole pieces of 16 bytes per row: a tensor store clips at those, not at
+  // the elements, and would write what lies behind a row that ends inside one.
+  const bool tma = !p.swap && p.tn % (128 / es) == 0 && aligned(y, 16) && (size_t)n * es % 16 == 0 && (size_t)ldy * es % 16 == 0 &&
+                   (size_t)ldy * es < (1ULL << 40);
   if (tma) {
     cuuint64_t dims[2] = {(cuuint64_t)n, (cuuint64_t)tokens};
     cuuint64_t strides[1] = {(cuuint64_t)ldy * es};

@@ -197,6 +197,21 @@ def test_linear_i8_of_several_tiles_per_sm(tokens, n, k, out):
     assert bool((big == 7.0).all())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("tokens,n,ld", [(129, 543, 544), (300, 11, 12), (700, 715, 728), (2500, 6003, 6008), (65, 1, 8)])
+def test_linear_i8_rows_that_end_inside_16_bytes(tokens, n, ld, out):
+    """Rows start on 16 bytes, but hold no whole number of them: the columns
+    behind them stay as they were."""
+    x, xs, w, ws = _product(tokens, n, 160)
+    ref = (x.double() @ w.double().t()) * xs.double()[:, None] * ws.double()
+    big = torch.full((tokens + 1, ld), 7.0, dtype=DT[out], device="cuda")
+    y = fm.linear_i8(x, xs, w, ws, out=big[:tokens, :n])
+    assert bool(((y.double() - ref).abs() <= ref.abs() * (3 * 2.0 ** -24 + HALF_ULP[out])).all())
+    y.fill_(7.0)
+    assert bool((big == 7.0).all())
+
+
 # -------------------------------------------------------------------- wide rows
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
