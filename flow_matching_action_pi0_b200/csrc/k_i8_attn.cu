@@ -43,8 +43,8 @@
 // out evenly: block i of G takes units [T i / G, T (i + 1) / G), whatever the
 // lengths, so a batch of ragged sequences finishes together (an equal number
 // of splits per sequence left the SMs to the longest ones: 36.8 us for 48
-// sequences of up to 8192 keys, 31.5 now, 3.3 TB/s).  Inside a block each warp has statistics of
-// its own and the warps meet once per sequence.  A sequence that lies in one
+// sequences of up to 8192 keys, 33 now, 3.1 TB/s).  Inside a block each warp has
+// statistics of its own and the warps meet once per sequence.  A sequence that lies in one
 // block is written out by it; of the others each block parks its fp32 rows in
 // one of its two workspace slots (0: the part continues an earlier block's, 1:
 // it begins here), and k_kv8_merge_few joins them.
@@ -661,7 +661,9 @@ cudaError_t merge_launch(const Kv8AttnPlan& p, const Kv8AttnArgs& a, cudaStream_
 
 // Two forms: groups of 8 rows (query heads of a KV head x queries) on mma.sync,
 // which read the cache once per group, and tiles of 128 rows on the tcgen05
-// tensor cores (fresh keys always), whose keys are split until the CTAs fill
+// tensor cores (fresh keys always, the groups have no place for them: one query and
+// one fresh key over 968 keys 11.7 us; 11.2 when the key is written to the cache
+// first, 48 sequences 21.7 and 18.9), whose keys are split until the CTAs fill
 // the SMs, each split keeping at least 64 keys of a full cache (one sequence of
 // 968 keys and 400 rows: 12.6 us; 14.8 with at least 128, 20.2 with 256).
 // Measured over 1 to 32 sequences of 256 to 16384 keys, 8 to 256 rows, head_dim d:
