@@ -387,10 +387,11 @@ pae_status pae_quantize_rows(const void* x, long long ldx, int rows, int width, 
                              signed char* codes, float* scale, pae_stream stream);
 
 /* y[t][f] = (sum_k x[t][k] w[f][k]) x_scale[t] w_scale[f]: x [tokens][k], w
- * [n][k] 8-bit codes (16-byte aligned), exact 32-bit sums, y [tokens][n] with
- * row stride ldy >= n in PAE_FP32 or PAE_BF16 (rounded once).  k a multiple of
- * 16, at most 131056, tokens and n at most 2^24 (else PAE_ERR_UNSUPPORTED);
- * tokens == 0 is a no-op. */
+ * [n][k] 8-bit codes (16-byte aligned), exact 32-bit sums, their conversion and
+ * the two products in fp32, y [tokens][n] with row stride ldy >= n in PAE_FP32 or
+ * PAE_BF16; what lies between its rows stays as it was.  k a multiple of 16, at
+ * most 131056, tokens and n at most 2^24 (else PAE_ERR_UNSUPPORTED); tokens == 0
+ * is a no-op. */
 pae_status pae_linear_i8(const signed char* x, const float* x_scale, const signed char* w, const float* w_scale,
                          int tokens, int n, int k, void* y, long long ldy, int dtype, pae_stream stream);
 
