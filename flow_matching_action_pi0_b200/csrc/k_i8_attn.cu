@@ -18,12 +18,13 @@
 //   c_j = exp2(s_j + log2 vs_j - ref) = p_j vs_j 2^(m - ref),
 // so that c in fp16 (rounded once, to 11 bits) is in units of the row's largest
 // contribution whatever the scales are: max c lies in [2^7, 2^15], so the steps of
-// 2^-24 at fp16's bottom put each contribution off by at most 2^-32 of the largest,
-// and the n keys of a warp's share by n 2^-32 at worst (all of them below the
-// step: the row sum counts what they lose).  The row sums have a reference m of their own, since a key may weigh much and
-// carry little: sum p_j in fp32, lane by lane.  The two meet in the exponent of
-// the row's last factor, 2^(ref - m) / sum, and partial rows are parked as
-// averages with the logarithm of their weight, so no size of V overflows or is lost.
+// 2^-24 at fp16's bottom put each contribution off by at most 2^-32 of the
+// largest, and the n keys of a warp's share by n 2^-32 at worst (all of them below
+// the step: the row sum counts what they lose).  The row sums have a reference m
+// of their own, since a key may weigh much and carry little: sum p_j in fp32, lane
+// by lane.  The two meet in the exponent of the row's last factor, 2^(ref - m) /
+// sum, and partial rows are parked as averages with the logarithm of their weight,
+// so no size of V overflows or is lost.
 //
 // Bound: bytes of the cache (2 (d + 4) per key and KV head).  The G query
 // heads of a KV head share every byte, 8 rows at a time as the N side of
@@ -38,16 +39,16 @@
 //   V: lane (g, t) loads 16 channels [128 h + 16 g, +16) of keys 2t, 2t + 1,
 //      2t + 8, 2t + 9; product m of block h takes channels 2 m (row g) and
 //      2 m + 1 (row g + 8)
-// Work is cut into units of 64 keys (16 per warp) of one (sequence, KV head,
-// row group); every sequence has one at least.  Units in that order are dealt
-// out evenly: block i of G takes units [T i / G, T (i + 1) / G), whatever the
-// lengths, so a batch of ragged sequences finishes together (an equal number
-// of splits per sequence left the SMs to the longest ones: 36.8 us for 48
-// sequences of up to 8192 keys, 33 now, 3.1 TB/s).  Inside a block each warp has
-// statistics of its own and the warps meet once per sequence.  A sequence that lies in one
-// block is written out by it; of the others each block parks its fp32 rows in
-// one of its two workspace slots (0: the part continues an earlier block's, 1:
-// it begins here), and k_kv8_merge_few joins them.
+// Work is cut into units of 64 keys (16 per warp) of one (sequence, KV head, row
+// group); every sequence has one at least.  Units in that order are dealt out
+// evenly: block i of G takes units [T i / G, T (i + 1) / G), whatever the lengths,
+// so a batch of ragged sequences finishes together (an equal number of splits per
+// sequence left the SMs to the longest ones: 36.8 us for 48 sequences of up to
+// 8192 keys, 33 now, 3.1 TB/s).  Inside a block each warp has statistics of its
+// own and the warps meet once per sequence.  A sequence that lies in one block is
+// written out by it; of the others each block parks its fp32 rows in one of its
+// two workspace slots (0: the part continues an earlier block's, 1: it begins
+// here), and k_kv8_merge_few joins them.
 #include <algorithm>
 #include <cmath>
 
